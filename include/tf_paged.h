@@ -213,6 +213,45 @@ TF_API int tf_paged_attn_prompt(const tf_kv_pool *pool, const tf_streams *stream
                          float scale, float *out, void *workspace,
                          size_t workspace_bytes, void *stream);
 
+/* Sliding-window attention with sinks: the layers of a model that see only
+ * the near context (TensorFold #1620 keeps such layers in ring caches of
+ * their own and pages only the full layers; here both read pages).  A row at
+ * position p sees the positions j <= p with
+ *     j > p - window   (the last `window` positions, its own included), or
+ *     j < sinks        (the stream's first tokens, which stay visible);
+ * the output is softmax(scale * q . k) weighted sum of v over them.  A row
+ * always sees itself.
+ *  window  >= 1; a window at or past max_len is the plain causal rule
+ *  sinks   >= 0
+ * rows, layouts, results and errors are those of tf_paged_attn_decode,
+ * _verify (rows in [1, 8]) and _prompt (rows in [1, 4096]), for every head
+ * dim, ratio of heads and page size.  Table entries and pool slots of
+ * positions that no row of the call sees are never read: pages wholly behind
+ * the window (tf_kv_pages_free_window) may hold -1 or belong to somebody
+ * else.  TF_EUNSUPPORTED for pools of more than 2^31 - 1 rows (n_pages *
+ * n_kv_heads * page_size).  The workspace is sized by its own call, since a
+ * window may be split over other kernels than the whole context; one
+ * workspace of the larger size serves both kinds of layer in turn. */
+TF_API size_t tf_paged_attn_window_workspace_bytes(const tf_kv_pool *pool,
+                                                   const tf_streams *streams,
+                                                   int32_t n_q_heads, int32_t rows,
+                                                   int32_t window, int32_t sinks);
+
+TF_API int tf_paged_attn_decode_window(const tf_kv_pool *pool, const tf_streams *streams,
+                                       const void *q, int32_t n_q_heads, int32_t window,
+                                       int32_t sinks, float scale, float *out, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+TF_API int tf_paged_attn_verify_window(const tf_kv_pool *pool, const tf_streams *streams,
+                                       const void *q, int32_t n_q_heads, int32_t rows,
+                                       int32_t window, int32_t sinks, float scale, float *out,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
+TF_API int tf_paged_attn_prompt_window(const tf_kv_pool *pool, const tf_streams *streams,
+                                       const void *q, int32_t n_q_heads, int32_t rows,
+                                       int32_t window, int32_t sinks, float scale, float *out,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+
 /* Single-row decode that allocates nothing and takes no workspace.  The
  * source pages have no counterpart of this call.
  * For callers that cannot allocate device memory for a workspace: a

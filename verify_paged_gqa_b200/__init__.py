@@ -13,6 +13,8 @@ _EXPORTS = (
     "tf_kv_copy_state", "tf_kv_put_rows", "tf_paged_attn_decode", "tf_paged_attn_prompt", "tf_paged_attn_verify",
     "tf_paged_attn_verify_tree", "tf_paged_attn_workspace_bytes", "tf_status_str",
     "tf_workspace_status", "tf_testing_paged_attn",
+    "tf_paged_attn_decode_window", "tf_paged_attn_verify_window", "tf_paged_attn_prompt_window",
+    "tf_paged_attn_window_workspace_bytes",
 )
 __all__ = list(_EXPORTS)
 

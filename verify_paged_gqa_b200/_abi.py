@@ -84,6 +84,16 @@ for _name in ("tf_paged_attn_verify", "tf_paged_attn_prompt"):
 raw.tf_paged_attn_verify_tree.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _i32, _i32, _vp,
                                           _f32, _vp, _vp, _sz, _vp]
 raw.tf_paged_attn_verify_tree.restype = ctypes.c_int
+raw.tf_paged_attn_window_workspace_bytes.argtypes = [_P(tf_kv_pool), _P(tf_streams), _i32, _i32,
+                                                     _i32, _i32]
+raw.tf_paged_attn_window_workspace_bytes.restype = _sz
+raw.tf_paged_attn_decode_window.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _i32, _i32, _i32,
+                                            _f32, _vp, _vp, _sz, _vp]
+raw.tf_paged_attn_decode_window.restype = ctypes.c_int
+for _name in ("tf_paged_attn_verify_window", "tf_paged_attn_prompt_window"):
+    getattr(raw, _name).argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _i32, _i32, _i32, _i32,
+                                    _f32, _vp, _vp, _sz, _vp]
+    getattr(raw, _name).restype = ctypes.c_int
 raw.tf_kv_copy_state.argtypes = [_P(tf_kv_pool), _P(tf_streams), _P(tf_kv_pool), _vp, _i32, _vp,
                                  _vp]
 raw.tf_kv_copy_state.restype = ctypes.c_int
@@ -183,7 +193,7 @@ def tf_paged_attn_workspace_bytes(k_pool, v_pool, table, lens, n_q_heads, rows, 
 
 
 def _attn(fn, name, k_pool, v_pool, table, lens, q, scale, out, workspace, max_len, stream,
-          with_rows, tree=None):
+          with_rows, tree=None, window=()):
     _need(q, torch.bfloat16, 4, "q")
     _need(out, torch.float32, 4, "out")
     if tuple(out.shape) != tuple(q.shape):
@@ -197,6 +207,7 @@ def _attn(fn, name, k_pool, v_pool, table, lens, q, scale, out, workspace, max_l
         args.append(q.shape[1])
     if tree is not None:
         args.append(tree.data_ptr())
+    args += window
     args += [float(scale), out.data_ptr(), workspace.data_ptr(), ws_bytes, _stream(stream)]
     _check(fn(*args), name)
     return out
@@ -236,6 +247,46 @@ def tf_paged_attn_prompt(k_pool, v_pool, table, lens, q, scale, out, workspace, 
     """A causal chunk of q.shape[1] prompt rows per stream (the last rows of each stream)."""
     return _attn(raw.tf_paged_attn_prompt, "tf_paged_attn_prompt", k_pool, v_pool, table, lens,
                  q, scale, out, workspace, max_len, stream, with_rows=True)
+
+
+def tf_paged_attn_window_workspace_bytes(k_pool, v_pool, table, lens, n_q_heads, rows, window,
+                                         sinks, max_len) -> int:
+    pool, st = _pool(k_pool, v_pool), _streams(table, lens, max_len)
+    n = raw.tf_paged_attn_window_workspace_bytes(ctypes.byref(pool), ctypes.byref(st), n_q_heads,
+                                                 rows, int(window), int(sinks))
+    if n == 0:
+        raise TFError(TF_EINVAL, "tf_paged_attn_window_workspace_bytes")
+    return int(n)
+
+
+def tf_paged_attn_decode_window(k_pool, v_pool, table, lens, q, window, sinks, scale, out,
+                                workspace, max_len, stream=None):
+    """One query row per stream (q [S][1][Hq][d]) that sees the last ``window``
+    positions and the first ``sinks`` ones."""
+    if q.shape[1] != 1:
+        raise ValueError("decode takes one row per stream")
+    return _attn(raw.tf_paged_attn_decode_window, "tf_paged_attn_decode_window", k_pool, v_pool,
+                 table, lens, q, scale, out, workspace, max_len, stream, with_rows=False,
+                 window=(int(window), int(sinks)))
+
+
+def tf_paged_attn_verify_window(k_pool, v_pool, table, lens, q, window, sinks, scale, out,
+                                workspace, max_len, stream=None):
+    """A causal draft window of q.shape[1] <= 8 rows per stream, each row
+    seeing the last ``window`` positions and the first ``sinks`` ones."""
+    return _attn(raw.tf_paged_attn_verify_window, "tf_paged_attn_verify_window", k_pool, v_pool,
+                 table, lens, q, scale, out, workspace, max_len, stream, with_rows=True,
+                 window=(int(window), int(sinks)))
+
+
+def tf_paged_attn_prompt_window(k_pool, v_pool, table, lens, q, window, sinks, scale, out,
+                                workspace, max_len, stream=None):
+    """A chunk of q.shape[1] prompt rows per stream (the last rows of each
+    stream), each row seeing the last ``window`` positions and the first
+    ``sinks`` ones."""
+    return _attn(raw.tf_paged_attn_prompt_window, "tf_paged_attn_prompt_window", k_pool, v_pool,
+                 table, lens, q, scale, out, workspace, max_len, stream, with_rows=True,
+                 window=(int(window), int(sinks)))
 
 
 def tf_testing_paged_attn(k_pool, v_pool, table, lens, q, scale, out, workspace, max_len,

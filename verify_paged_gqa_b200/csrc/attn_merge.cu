@@ -24,8 +24,8 @@ namespace tfp {
 
 constexpr int kMergeRows = 8;    // rows (warps) per merge block
 
-template <int D>
-__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ AttnParams p)
+template <int D, class P>
+__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ P p)
 {
     constexpr int DL = D / 32;            // output floats per lane
     constexpr int NV = DL / 4;            // float4 per lane and segment
@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
     }
 }
 
-template <int D>
-cudaError_t launch_attn_merge(const AttnParams &p, cudaStream_t stream)
+template <int D, class P>
+cudaError_t launch_attn_merge(const P &p, cudaStream_t stream)
 {
     const int groups = (p.RB + kMergeRows - 1) / kMergeRows;
     const int64_t blocks = (int64_t)p.S * p.Hkv * p.n_rblk * groups;
@@ -222,12 +222,15 @@ cudaError_t launch_attn_merge(const AttnParams &p, cudaStream_t stream)
     const int threads = 32 * min(kMergeRows, p.RB);
     // programmatic dependent launch: the blocks are scheduled while the
     // partial kernel runs out and wait for it in the kernel
-    return launch_dependent(attn_merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(threads),
+    return launch_dependent(attn_merge_kernel<D, P>, dim3(static_cast<unsigned>(blocks)), dim3(threads),
                             0, stream, p);
 }
 
 template cudaError_t launch_attn_merge<128>(const AttnParams &, cudaStream_t);
+template cudaError_t launch_attn_merge<128>(const WinParams &, cudaStream_t);
 template cudaError_t launch_attn_merge<256>(const AttnParams &, cudaStream_t);
+template cudaError_t launch_attn_merge<256>(const WinParams &, cudaStream_t);
 template cudaError_t launch_attn_merge<512>(const AttnParams &, cudaStream_t);
+template cudaError_t launch_attn_merge<512>(const WinParams &, cudaStream_t);
 
 }  // namespace tfp

@@ -131,9 +131,9 @@ static_assert(pm_smem_bytes<512, 32>() <= kSmemCap, "smem");
 
 // Kernel arguments: the call's parameters and the K and V pools' tensor maps
 // (one 128-row box, or for tiles assembled from pages one map per box height).
-template <bool kG>
+template <bool kG, class P>
 struct PmArgs {
-    AttnParams p;
+    P p;
     CUtensorMap kmap[kG ? kBoxHeights : 1];
     CUtensorMap vmap[kG ? kBoxHeights : 1];
 };
@@ -212,7 +212,7 @@ template <int D, int NR, class A>
 __device__ __forceinline__ void pm_issuer(const A &a, PmSmem<D, NR> &sm)
 {
     using C = PmCfg<D, NR>;
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const uint32_t tmem = sm.tmem_base;
     constexpr uint32_t idPV = f16_idesc(128, 2 * NR, 1, 1);
     const uint32_t ring0 = smem_addr(sm.ring[0]);
@@ -276,11 +276,15 @@ __device__ __forceinline__ void pm_issuer(const A &a, PmSmem<D, NR> &sm)
     (void)mbar_wait(&sm.fin, 0, sm.wait_limit);
 }
 
+// Which rows of a block see a position: causal windows, tree masks, or
+// sliding windows with sinks.
+enum PmMask { kCausal, kTreeMask, kWindow };
+
 // Whether the thread's row R0 + r sees its position (see the tile loop).
-template <bool kTree>
+template <PmMask kMask>
 __device__ __forceinline__ bool pm_sees(int r, int rvis, uint32_t vis)
 {
-    if constexpr (kTree)
+    if constexpr (kMask != kCausal)
         return ((vis >> r) & 1u) != 0;
     else
         return r >= rvis;
@@ -295,7 +299,7 @@ template <int D, int NR, class A>
 __device__ __forceinline__ void pm_producer_dual(const A &a, PmSmem<D, NR> &sm)
 {
     using C = PmCfg<D, NR>;
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const uint64_t pol = l2_evict_first_policy();
     uint32_t UK = 0, UV = 0;
     bool ok = true;
@@ -372,7 +376,7 @@ template <int D, int NR, class A>
 __device__ __forceinline__ void pm_producer_dual_pieces(const A &a, PmSmem<D, NR> &sm, int lane)
 {
     using C = PmCfg<D, NR>;
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const uint64_t pol = l2_evict_first_policy();
     uint32_t UK = 0, UV = 0;  // units issued
     bool ok = true;
@@ -385,8 +389,8 @@ __device__ __forceinline__ void pm_producer_dual_pieces(const A &a, PmSmem<D, NR
         // rows and page ids of tiles t, t + 1 and t + 2 (the page ids are read
         // two tiles before their first use)
         auto nvalid = [&](int t) { return min(PT, it.len - (it.key0 + t * PT)); };
-        TilePages t0 = tile_pages(p, trow, it.key0, nvalid(0), lane);
-        TilePages t1 = n > 1 ? tile_pages(p, trow, it.key0 + PT, nvalid(1), lane) : t0;
+        auto t0 = tile_pages(p, it, trow, it.key0, nvalid(0), lane);
+        auto t1 = n > 1 ? tile_pages(p, it, trow, it.key0 + PT, nvalid(1), lane) : t0;
 #pragma unroll 1
         for (int kb = 0; ok && kb < C::DB; ++kb) {
             ok = pieces_unit(p, sm, (int)(UK % C::NK), ((UK / C::NK) & 1u) ^ 1u, a.kmap, t0, trow,
@@ -395,8 +399,8 @@ __device__ __forceinline__ void pm_producer_dual_pieces(const A &a, PmSmem<D, NR
         }
         for (int t = 0; ok && t < n; ++t) {
             const int pos = it.key0 + t * PT;
-            const TilePages t2 =
-                t + 2 < n ? tile_pages(p, trow, pos + 2 * PT, nvalid(t + 2), lane) : t1;
+            const auto t2 =
+                t + 2 < n ? tile_pages(p, it, trow, pos + 2 * PT, nvalid(t + 2), lane) : t1;
 #pragma unroll 1
             for (int kb = 0; ok && kb < C::DB; ++kb) {
                 if (t + 1 < n) {
@@ -431,7 +435,7 @@ template <int D, int NR, class A>
 __device__ __forceinline__ void pm_qk_issuer(const A &a, PmSmem<D, NR> &sm)
 {
     using C = PmCfg<D, NR>;
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const uint32_t tmem = sm.tmem_base;
     const uint32_t ring0 = smem_addr(sm.ring[0]);
     const uint32_t q0 = smem_addr(sm.q);
@@ -468,7 +472,7 @@ template <int D, int NR, class A>
 __device__ __forceinline__ void pm_pv_issuer(const A &a, PmSmem<D, NR> &sm, int lane)
 {
     using C = PmCfg<D, NR>;
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const uint32_t tmem = sm.tmem_base;
     constexpr uint32_t idPV = f16_idesc(128, 2 * NR, 1, 1);
     const uint32_t pt0 = smem_addr(sm.pt[0]);
@@ -484,6 +488,7 @@ __device__ __forceinline__ void pm_pv_issuer(const A &a, PmSmem<D, NR> &sm, int 
                 ok = pwait(sm, &sm.p_full[T & 1u], (T >> 1) & 1u, p.flags, kWaitQEmpty);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             const int nvalid = it.len - (it.key0 + t * PT);
+            const TileRows rows = tile_rows(p, it, it.key0 + t * PT, min(nvalid, PT));
             const uint32_t pb = pt0 + (T % C::kPBufs) * C::kPBytes;
 #pragma unroll 1
             for (int vb = 0; ok && vb < C::DB; ++vb, ++UV) {
@@ -493,7 +498,7 @@ __device__ __forceinline__ void pm_pv_issuer(const A &a, PmSmem<D, NR> &sm, int 
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok)
                 break;
-            if (nvalid < PT) {
+            if (nvalid < PT || rows.a < rows.b) {
                 // every lane acquires the landed unit (its phase is complete and
                 // cannot move on before this warp releases the slot)
                 (void)mbar_wait(&sm.full[st], (UV / C::NV) & 1u, sm.wait_limit);
@@ -501,6 +506,11 @@ __device__ __forceinline__ void pm_pv_issuer(const A &a, PmSmem<D, NR> &sm, int 
                 for (int f = lane; f < (PT - nvalid) * 16; f += 32)
                     *reinterpret_cast<uint4 *>(sm.ring[st] + ((f >> 3) & 1) * kBox +
                                                sw128_off(nvalid + (f >> 4), f & 7)) =
+                        make_uint4(0, 0, 0, 0);
+                // and the rows between the sinks and the window
+                for (int f = lane; f < (rows.b - rows.a) * 16; f += 32)
+                    *reinterpret_cast<uint4 *>(sm.ring[st] + ((f >> 3) & 1) * kBox +
+                                               sw128_off(rows.a + (f >> 4), f & 7)) =
                         make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 __syncwarp();
@@ -531,12 +541,13 @@ __device__ __forceinline__ void pm_pv_issuer(const A &a, PmSmem<D, NR> &sm, int 
 // NW = 4 * NR / 32 softmax warps: warp w reads tensor-memory lanes
 // 32 * (w % 4) .. + 31 (tile positions, or O^T dims), and owns the 32 rows
 // [32 h, 32 h + 32) with h = (w - 2) / 4.
-template <int D, int NR, bool kTree, class A>
+template <int D, int NR, PmMask kMask, class A>
 __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int warp, int lane)
 {
     using C = PmCfg<D, NR>;
     constexpr int NT = C::kSoftThreads;
-    const AttnParams &p = a.p;
+    constexpr bool kTree = kMask == kTreeMask;
+    const auto &p = a.p;
     const int wq = warp & 3;             // tensor-memory lane quarter of this warp
     const int h = (warp - 2) >> 2;       // row half: rows [32 h, 32 h + 32)
     const int tid = wq * 32 + lane;      // position in the tile; O^T lane (dim within a block)
@@ -648,21 +659,38 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
         // the block's first row sees the fewest positions (under tree masks,
         // every row sees the positions before the window)
         const int lim_lo = kTree ? it.len - p.W : row_lim(p, it.len, it.b * NR);
+        // sliding window: the block's last row starts latest
+        int start_hi = 0, sinks = 0;
+        if constexpr (kMask == kWindow) {
+            start_hi = row_lim(p, it.len, it.b * NR + NR - 1) - p.window;
+            sinks = p.sinks;
+        }
         for (int t = 0; t < n; ++t) {
             const uint32_t u = u0 + t;
             const int tpos = it.key0 + t * PT;
             const uint32_t tS = lane_base + C::kColS + (u & 1u) * NR + R0;
             // a tile every row of the block sees whole needs no mask
-            const bool whole = tpos + PT <= lim_lo && tpos + PT <= it.key1;
+            const bool whole = tpos + PT <= lim_lo && tpos + PT <= it.key1 &&
+                               (kMask != kWindow || tpos >= start_hi || tpos + PT <= sinks);
             // causal: rows R0 + r, r >= rvis, see this thread's position;
             // tree: row R0 + r sees it when bit r of vis is set
             const int pos = tpos + tid;
             const int rvis = kTree || pos >= it.key1 || pos >= it.len
                                  ? 32
                                  : p.G * max(0, pos - (it.len - p.W)) - it.b * NR - R0;
-            const uint32_t vis = !kTree || pos >= it.key1 || pos >= it.len ? 0u
-                                 : pos < it.len - p.W                     ? 0xffffffffu
-                                                       : sm.rowvis[h][pos - (it.len - p.W)];
+            uint32_t vis = !kTree || pos >= it.key1 || pos >= it.len ? 0u
+                           : pos < it.len - p.W                     ? 0xffffffffu
+                                                 : sm.rowvis[h][pos - (it.len - p.W)];
+            if constexpr (kMask == kWindow) {
+                // rows R0 + r, rvis <= r < rend: window row w sees pos when
+                // pos > len - W + w - window, i.e. w < window - back
+                const int back = it.len - p.W - pos;
+                const int rend = pos < sinks || back <= p.window - p.W ? 32
+                                 : back >= p.window ? 0
+                                                    : p.G * (p.window - back) - it.b * NR - R0;
+                vis = (rvis >= 32 ? 0u : rvis <= 0 ? 0xffffffffu : 0xffffffffu << rvis) &
+                      (rend >= 32 ? 0xffffffffu : rend <= 0 ? 0u : (1u << rend) - 1u);
+            }
             ok = pwait(sm, &sm.s_full[u & 1u], (u >> 1) & 1u, p.flags, kWaitFull) && ok;
             tc_fence_after();
 
@@ -682,7 +710,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 if (!whole) {
 #pragma unroll
                     for (int r = 0; r < 32; ++r)
-                        x[r] = pm_sees<kTree>(r, rvis, vis) ? x[r] : NEG_INF;
+                        x[r] = pm_sees<kMask>(r, rvis, vis) ? x[r] : NEG_INF;
                 }
                 mx = max_tree(x);
                 slow = block_any<NT>(mx > kRescaleLog2);
@@ -693,7 +721,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 load_scores<32>(tS, y);
 #pragma unroll
                 for (int r = 0; r < 32; ++r)
-                    y[r] = (whole || pm_sees<kTree>(r, rvis, vis)) ? y[r] * sl : NEG_INF;
+                    y[r] = (whole || pm_sees<kMask>(r, rvis, vis)) ? y[r] * sl : NEG_INF;
                 xpose_reduce<32, true>(y, lane);
                 sm.red[wq][R0 + lane] = y[0];
                 named_barrier(1, NT);
@@ -748,12 +776,13 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 if (!whole) {
 #pragma unroll
                     for (int r = 0; r < 32; ++r)
-                        x[r] = pm_sees<kTree>(r, rvis, vis) ? x[r] : NEG_INF;
+                        x[r] = pm_sees<kMask>(r, rvis, vis) ? x[r] : NEG_INF;
                 }
             }
             // --- V rows past the stream's end: zero them (0 * NaN = NaN) ----
             const int nvalid = it.len - tpos;
-            if (!C::kDual && nvalid < PT) {
+            const TileRows rows = tile_rows(p, it, tpos, min(nvalid, PT));
+            if (!C::kDual && (nvalid < PT || rows.a < rows.b)) {
                 // The ring slots of this tile's V units last held units of
                 // V(t - 1) or earlier (at head dim 512 the ring is shorter than
                 // a tile): wait for PV(u - 1) first, so each full-barrier wait
@@ -761,13 +790,19 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 if (u >= 1)
                     ok = pwait(sm, &sm.o_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u, p.flags,
                                kWaitEmpty) && ok;
+                // (a sliding window has such rows in inner tiles too, where the
+                // slots may have held units of K(t + 1): QK(u + 1) needs no P of
+                // this tile, so wait for it as well)
+                if (kMask == kWindow && t + 1 < n)
+                    ok = pwait(sm, &sm.s_full[(u + 1) & 1u], ((u + 1) >> 1) & 1u, p.flags,
+                               kWaitFull) && ok;
                 // the V units of this tile: K(0), then per tile K(t + 1) if any, V(t)
                 uint32_t uv = ring_v_unit(C::DB, u0, t, n);
 #pragma unroll 1
                 for (int vb = 0; vb < C::DB; ++vb, ++uv) {
                     const int sl8 = (int)(uv % C::NU);
                     ok = pwait(sm, &sm.full[sl8], (uv / C::NU) & 1u, p.flags, kWaitFull) && ok;
-                    if (tid >= nvalid) {
+                    if (tid >= nvalid || (tid >= rows.a && tid < rows.b)) {
                         // the NW / 4 threads of a position split the unit's two boxes
 #pragma unroll 1
                         for (int bx = h; bx < 2; bx += NR / 32) {
@@ -787,12 +822,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 const float p1 = fast_exp2(x[2 * e + 1]);
                 l[2 * e] += p0;
                 l[2 * e + 1] += p1;
-                // P = hi + lo, both bf16 by truncation: |p - hi - lo| < 2^-14 p
-                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-                hw[e] = __byte_perm(b0, b1, 0x7632);
-                const float r0 = p0 - __uint_as_float(b0 & 0xffff0000u);
-                const float r1 = p1 - __uint_as_float(b1 & 0xffff0000u);
-                lw[e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+                split_p<kMask == kWindow>(p0, p1, hw[e], lw[e]);
             }
             // buffer u % kPBufs is free once PV(u - kPBufs) completed
             if (u >= (uint32_t)C::kPBufs) {
@@ -878,9 +908,9 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
     }
 }
 
-template <int D, int NR, bool kTree, bool kG>
+template <int D, int NR, PmMask kMask, bool kG, class P>
 __global__ void __launch_bounds__(PmCfg<D, NR>::kThreads, 1)
-    attn_pm_kernel(const __grid_constant__ PmArgs<kG> a)
+    attn_pm_kernel(const __grid_constant__ PmArgs<kG, P> a)
 {
     using C = PmCfg<D, NR>;
     extern __shared__ uint8_t smem_raw[];
@@ -946,7 +976,7 @@ __global__ void __launch_bounds__(PmCfg<D, NR>::kThreads, 1)
     } else if (C::kDual && warp == C::kPvWarp) {
         pm_pv_issuer<D, NR>(a, sm, lane);
     } else {
-        pm_softmax<D, NR, kTree>(a, sm, warp, lane);
+        pm_softmax<D, NR, kMask>(a, sm, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -958,10 +988,10 @@ __global__ void __launch_bounds__(PmCfg<D, NR>::kThreads, 1)
     }
 }
 
-template <int D, int NR, bool kTree, bool kG>
-cudaError_t launch_pm(const AttnParams &p, int grid, cudaStream_t stream)
+template <int D, int NR, PmMask kMask, bool kG, class P>
+cudaError_t launch_pm(const P &p, int grid, cudaStream_t stream)
 {
-    PmArgs<kG> a;
+    PmArgs<kG, P> a;
     a.p = p;
     // one box of a whole 128-position tile, or boxes of 1, 2, 4, ..., 128 rows
     // for tiles assembled from page pieces
@@ -973,10 +1003,10 @@ cudaError_t launch_pm(const AttnParams &p, int grid, cudaStream_t stream)
     }
     static std::atomic<bool> configured[kMaxDevices];
     constexpr size_t bytes = pm_smem_bytes<D, NR>();
-    const cudaError_t e = set_smem_limit_once(attn_pm_kernel<D, NR, kTree, kG>, bytes, configured);
+    const cudaError_t e = set_smem_limit_once(attn_pm_kernel<D, NR, kMask, kG, P>, bytes, configured);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(attn_pm_kernel<D, NR, kTree, kG>, dim3(grid),
+    return launch_dependent(attn_pm_kernel<D, NR, kMask, kG, P>, dim3(grid),
                             dim3(PmCfg<D, NR>::kThreads), bytes, stream, a);
 }
 
@@ -998,17 +1028,17 @@ int pm_rows(const AttnParams &p)
     return 0;
 }
 
-template <bool kTree, bool kG>
-cudaError_t launch_attn_pm_t(const AttnParams &p, int grid, cudaStream_t stream)
+template <PmMask kMask, bool kG, class P>
+cudaError_t launch_attn_pm_t(const P &p, int grid, cudaStream_t stream)
 {
     if (p.D == 128 && p.RB == 32)
-        return launch_pm<128, 32, kTree, kG>(p, grid, stream);
+        return launch_pm<128, 32, kMask, kG>(p, grid, stream);
     if (p.D == 128 && p.RB == 64)
-        return launch_pm<128, 64, kTree, kG>(p, grid, stream);
+        return launch_pm<128, 64, kMask, kG>(p, grid, stream);
     if (p.D == 256 && p.RB == 32)
-        return launch_pm<256, 32, kTree, kG>(p, grid, stream);
+        return launch_pm<256, 32, kMask, kG>(p, grid, stream);
     if (p.D == 512 && p.RB == 32)
-        return launch_pm<512, 32, kTree, kG>(p, grid, stream);
+        return launch_pm<512, 32, kMask, kG>(p, grid, stream);
     return cudaErrorInvalidValue;
 }
 
@@ -1018,10 +1048,18 @@ cudaError_t launch_attn_pm(const AttnParams &p, int grid, cudaStream_t stream)
 {
     const bool gather = p.P % PT != 0;
     if (p.has_tree)
-        return gather ? launch_attn_pm_t<true, true>(p, grid, stream)
-                      : launch_attn_pm_t<true, false>(p, grid, stream);
-    return gather ? launch_attn_pm_t<false, true>(p, grid, stream)
-                  : launch_attn_pm_t<false, false>(p, grid, stream);
+        return gather ? launch_attn_pm_t<kTreeMask, true>(p, grid, stream)
+                      : launch_attn_pm_t<kTreeMask, false>(p, grid, stream);
+    return gather ? launch_attn_pm_t<kCausal, true>(p, grid, stream)
+                  : launch_attn_pm_t<kCausal, false>(p, grid, stream);
+}
+
+// Sliding windows: the sinks and the window's first positions end and start
+// inside tiles, so tiles are assembled from pieces at any page size (a tile
+// that lies in one page is one box, as above).
+cudaError_t launch_attn_pm(const WinParams &p, int grid, cudaStream_t stream)
+{
+    return launch_attn_pm_t<kWindow, true>(p, grid, stream);
 }
 
 }  // namespace tfp

@@ -81,9 +81,9 @@ static_assert(kPrSmemBytes <= 232448, "shared memory");
 
 // Kernel arguments: the call's parameters and the K and V pools' tensor maps
 // (one 128-row box, or for tiles assembled from pages one map per box height).
-template <bool kG>
+template <bool kG, class P>
 struct PrArgs {
-    AttnParams p;
+    P p;
     CUtensorMap kmap[kG ? kBoxHeights : 1];
     CUtensorMap vmap[kG ? kBoxHeights : 1];
 };
@@ -120,7 +120,7 @@ __device__ __forceinline__ bool pr_qk(PrSmem &sm, uint32_t &U, uint32_t u, uint3
 template <class A>
 __device__ __forceinline__ void pr_issuer(const A &a, PrSmem &sm)
 {
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const uint32_t tmem = sm.tmem_base;
     // O^T += V^T P^T: A = V^T (MN-major, from the V unit), B = P (K-major,
     // [256 rows: hi then lo][positions]), N = 256
@@ -179,16 +179,22 @@ __device__ __forceinline__ void pr_issuer(const A &a, PrSmem &sm)
 
 // ---- softmax warps -----------------------------------------------------------
 
+// The low n of 64 bits (n of any value).
+__device__ __forceinline__ uint64_t low_bits(int n)
+{
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+}
+
 // Eight warps (2..9).  Warp w reads tensor-memory lanes 32 (w % 4) .. + 31
 // and owns half hh = (w - 2) / 4 of the tile: positions [64 hh, 64 hh + 64),
 // which are K-atom hh of the P tile.  During a tile a thread works on its
 // row's half; a row's two threads agree on the row's reference max (they
 // compute it from the same shared values).  In the epilogue the thread reads
 // O^T lane r (head dim r) for rows [64 hh, 64 hh + 64).
-template <class A>
+template <bool kWin, class A>
 __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int lane)
 {
-    const AttnParams &p = a.p;
+    const auto &p = a.p;
     const int wq = warp & 3;
     const int hh = (warp - 2) >> 2;
     const int r = wq * 32 + lane;
@@ -256,6 +262,14 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
         // positions this row sees, and the fewest any row of the block sees
         const int lim = min(row_lim(p, it.len, m), it.key1);
         const int lim_lo = min(row_lim(p, it.len, it.b * RR), it.key1);
+        // sliding window: the row's first position past the sinks, and the last
+        // row's, which starts latest
+        int start = 0, start_hi = 0, sinks = 0;
+        if constexpr (kWin) {
+            start = row_lim(p, it.len, m) - p.window;
+            start_hi = row_lim(p, it.len, it.b * RR + RR - 1) - p.window;
+            sinks = p.sinks;
+        }
         for (int t = 0; t < n; ++t) {
             const uint32_t u = u0 + t;
             const int tpos = it.key0 + t * PT;
@@ -280,7 +294,17 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             if (lane == 0)
                 mbar_arrive(&sm.s_free);
             // masked positions are selected to -inf (K rows there may be NaN)
-            if (hpos + 64 > lim_lo) {
+            if constexpr (kWin) {
+                if (hpos + 64 > lim_lo || (hpos < start_hi && hpos + 64 > sinks)) {
+                    // bits of the half's positions that the row sees
+                    const uint64_t sees = low_bits(lim - hpos) &
+                                          (~low_bits(start - hpos) | low_bits(sinks - hpos));
+                    const uint32_t s0 = (uint32_t)sees, s1 = (uint32_t)(sees >> 32);
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        s[k] = ((k < 32 ? s0 : s1) >> (k & 31)) & 1u ? s[k] : NEG_INF;
+                }
+            } else if (hpos + 64 > lim_lo) {
                 const int vis = lim - hpos;
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
@@ -327,11 +351,12 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             }
             // V rows past the stream's end are zeroed (0 * NaN = NaN): the two
             // threads of position r take one 64-dim box each
-            if (tpos + PT > it.len) {
+            const TileRows rows = tile_rows(p, it, tpos, min(it.len - tpos, PT));
+            if (tpos + PT > it.len || rows.a < rows.b) {
                 const uint32_t uv = ring_v_unit(1, u0, t, n);
                 const int st = (int)(uv % NU);
                 ok = pwait(sm, &sm.full[st], (uv / NU) & 1u, p.flags, kWaitFull) && ok;
-                if (r >= it.len - tpos) {
+                if (r >= it.len - tpos || (r >= rows.a && r < rows.b)) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         *reinterpret_cast<uint4 *>(sm.ring[st] + hh * kRingBox + sw128_off(r, c)) =
@@ -351,6 +376,10 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                     const float2 x = __ffma2_rn(make_float2(s[k], s[k + 1]), sl2, nm2);
                     const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                     lacc = __fadd2_rn(lacc, pp);
+                    if constexpr (kWin) {
+                        split_p<true>(pp.x, pp.y, hw[e], lw[e]);
+                        continue;
+                    }
                     // P = hi + lo, both bf16 by truncation: |p - hi - lo| < 2^-14 p
                     const uint32_t b0 = __float_as_uint(pp.x), b1 = __float_as_uint(pp.y);
                     hw[e] = __byte_perm(b0, b1, 0x7632);
@@ -421,8 +450,9 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
     }
 }
 
-template <bool kG>
-__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ PrArgs<kG> a)
+template <bool kG, bool kWin, class P>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ PrArgs<kG, P> a)
 {
     extern __shared__ uint8_t smem_raw[];
     PrSmem &sm = *reinterpret_cast<PrSmem *>(
@@ -472,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             pr_issuer(a, sm);
         __syncwarp();
     } else {
-        pr_softmax(a, sm, warp, lane);
+        pr_softmax<kWin>(a, sm, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -496,10 +526,10 @@ bool prompt_supported(const AttnParams &p)
     return p.D == DD && pool_rows_fit(p);
 }
 
-template <bool kG>
-cudaError_t launch_prompt(const AttnParams &p, int grid, cudaStream_t stream)
+template <bool kG, bool kWin, class P>
+cudaError_t launch_prompt(const P &p, int grid, cudaStream_t stream)
 {
-    PrArgs<kG> a;
+    PrArgs<kG, P> a;
     a.p = p;
     // one box of a whole 128-position tile, or boxes of 1, 2, 4, ..., 128 rows
     // for tiles assembled from page pieces
@@ -510,10 +540,10 @@ cudaError_t launch_prompt(const AttnParams &p, int grid, cudaStream_t stream)
             return cudaErrorInvalidValue;
     }
     static std::atomic<bool> configured[kMaxDevices];
-    const cudaError_t e = set_smem_limit_once(attn_prompt_kernel<kG>, kPrSmemBytes, configured);
+    const cudaError_t e = set_smem_limit_once(attn_prompt_kernel<kG, kWin, P>, kPrSmemBytes, configured);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(attn_prompt_kernel<kG>, dim3(grid), dim3(kThreads), kPrSmemBytes,
+    return launch_dependent(attn_prompt_kernel<kG, kWin, P>, dim3(grid), dim3(kThreads), kPrSmemBytes,
                             stream, a);
 }
 
@@ -521,8 +551,14 @@ cudaError_t launch_prompt(const AttnParams &p, int grid, cudaStream_t stream)
 // other page sizes assemble each tile from page pieces.
 cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t stream)
 {
-    return p.P % PT != 0 ? launch_prompt<true>(p, grid, stream)
-                         : launch_prompt<false>(p, grid, stream);
+    return p.P % PT != 0 ? launch_prompt<true, false>(p, grid, stream)
+                         : launch_prompt<false, false>(p, grid, stream);
+}
+
+// Sliding windows start and end inside tiles: pieces at any page size.
+cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream)
+{
+    return launch_prompt<true, true>(p, grid, stream);
 }
 
 }  // namespace tfp

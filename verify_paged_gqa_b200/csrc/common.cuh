@@ -68,6 +68,13 @@ struct AttnParams {
     float scale_log2;           // scale * log2(e): scores are kept in log2 units
 };
 
+// A sliding-window call: a row sees the last `window` positions up to its own
+// and the first `sinks` ones.  A type of its own, so that the plain calls'
+// kernels carry none of it.
+struct WinParams : AttnParams {
+    int32_t window, sinks;      // window >= 1, sinks >= 0, both at most max_len
+};
+
 // Floats per partial slot: SR rows of O (D floats each), then SR running
 // maxima and SR running sums, rounded up to 16 bytes so every slot (and every
 // row of O in it) starts 16-byte aligned.

@@ -88,18 +88,20 @@ template <int D>
 size_t simt_smem_bytes();
 template <int D>
 cudaError_t launch_attn_simt(const AttnParams &p, int grid, cudaStream_t stream);
-template <int D>
-cudaError_t launch_attn_merge(const AttnParams &p, cudaStream_t stream);  // D 128, 256, 512
+template <int D, class P>
+cudaError_t launch_attn_merge(const P &p, cudaStream_t stream);  // D 128, 256, 512
 
 // Prompt tensor-core partial kernel (tcgen05): row blocks of prompt_rows()
 // rows on the QK MMA's M, PV transposed.
 int prompt_rows();
 bool prompt_supported(const AttnParams &p);
 cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream);
 
 // Position-major tensor-core partial kernel: key positions on the MMA's M,
 // row blocks of pm_rows(p) rows (0: not supported for these arguments).
 int pm_rows(const AttnParams &p);
 cudaError_t launch_attn_pm(const AttnParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_attn_pm(const WinParams &p, int grid, cudaStream_t stream);
 
 }  // namespace tfp

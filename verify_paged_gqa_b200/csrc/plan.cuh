@@ -25,6 +25,16 @@
 // gives CTA c unit c whole: no partials and no merge.)  A unit's result
 // therefore depends on the lengths of the call's streams and the grid size
 // (never on the page table, nor on run-to-run timing).
+//
+// Sliding-window calls (WinParams): the rows of a block see the positions
+// [0, sinks) and [start, lim), where start is the first position of its first
+// row's window.  The unit then lives in squeezed positions: past the sinks,
+// block_skip positions are left out, the largest multiple of 128 that keeps
+// the two runs apart, so a squeezed position x >= sinks is position x + skip
+// and tiles keep their alignment to pages.  The up to 127 squeezed positions
+// in [sinks, start - skip) that no row sees are never loaded.  Everything a
+// kernel computes from (length, limits, tiles) is in squeezed positions; only
+// the page walk adds the skip.
 #pragma once
 
 #include "common.cuh"
@@ -39,14 +49,30 @@ __host__ __device__ __forceinline__ bool len_ok(const AttnParams &p, int len)
     return len >= p.W && len <= p.max_len && (int64_t)len <= (int64_t)p.table_stride * p.P;
 }
 
+// First position of the window of row block b's first row (it may be below 0).
+__host__ __device__ __forceinline__ int block_start(const WinParams &p, int len, int b)
+{
+    return len - p.W + b * p.RB / p.G - p.window + 1;
+}
+
+// Positions past the sinks that row block b's squeezed positions leave out.
+__host__ __device__ __forceinline__ int block_skip(const AttnParams &, int, int) { return 0; }
+
+__host__ __device__ __forceinline__ int block_skip(const WinParams &p, int len, int b)
+{
+    const int start = block_start(p, len, b);
+    return start > p.sinks ? (start - p.sinks) / kTile * kTile : 0;
+}
+
 // One past the last position any row of row block b may see (under tree
 // masks a row may see any row of its window).
-__host__ __device__ __forceinline__ int block_lim(const AttnParams &p, int len, int b)
+template <class P>
+__host__ __device__ __forceinline__ int block_lim(const P &p, int len, int b)
 {
     if (p.has_tree)
         return len;
     const int m_last = min(p.M, (b + 1) * p.RB) - 1;
-    return len - p.W + m_last / p.G + 1;
+    return len - p.W + m_last / p.G + 1 - block_skip(p, len, b);
 }
 
 // One past the position row m sees (rows past M are clamped to the last row);
@@ -56,20 +82,23 @@ __host__ __device__ __forceinline__ int row_lim(const AttnParams &p, int len, in
     return len - p.W + min(m, p.M - 1) / p.G + 1;
 }
 
-__host__ __device__ __forceinline__ int unit_tiles(const AttnParams &p, int len, int b)
+template <class P>
+__host__ __device__ __forceinline__ int unit_tiles(const P &p, int len, int b)
 {
     return (block_lim(p, len, b) + kTile - 1) / kTile;
 }
 
 // Work of a unit: its entry tiles, then its tiles.
-__host__ __device__ __forceinline__ int unit_work(const AttnParams &p, int len, int b)
+template <class P>
+__host__ __device__ __forceinline__ int unit_work(const P &p, int len, int b)
 {
     return p.VT + unit_tiles(p, len, b);
 }
 
 // Work of one KV head of a stream (all its row blocks); 0 for a length out
 // of range (those streams are skipped and reported by the merge kernel).
-__host__ __device__ __forceinline__ int64_t head_work(const AttnParams &p, int len)
+template <class P>
+__host__ __device__ __forceinline__ int64_t head_work(const P &p, int len)
 {
     if (!len_ok(p, len))
         return 0;
@@ -102,7 +131,8 @@ struct CtaRange {
 // time: the total work, then the stream holding the CTA's first work tile.
 // CTA 0 also records where every stream's work starts and the total in the
 // workspace for the merge kernel.
-__device__ __forceinline__ void find_range(const AttnParams &p, CtaRange &out, int lane)
+template <class P>
+__device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
 {
     if (p.whole) {
         // CTA c takes unit c (stream, KV head, row block) whole
@@ -176,7 +206,39 @@ struct WorkItem {
     int key0, key1;  // positions [key0, key1) this segment reads
     bool fin;        // covers the whole unit: write the rows' outputs
     int slot;        // partial slot otherwise
+    // sliding-window calls: len, key0 and key1 are squeezed; positions from
+    // `sink_end` on lie `skip` further on, and [sink_end, dead_end) is not loaded
+    int skip, sink_end, dead_end;
 };
+
+__device__ __forceinline__ void set_window(const AttnParams &, WorkItem &) {}
+
+__device__ __forceinline__ void set_window(const WinParams &p, WorkItem &w)
+{
+    const int start = block_start(p, w.len, w.b);
+    w.skip = block_skip(p, w.len, w.b);
+    w.sink_end = start > p.sinks ? p.sinks : INT32_MAX;  // (one run: no gap)
+    w.dead_end = start > p.sinks ? start - w.skip : 0;
+    w.len -= w.skip;
+}
+
+// The rows of a tile that are loaded: [0, a) and [b, nvalid).
+struct TileRows {
+    int a, b;
+};
+
+__device__ __forceinline__ TileRows tile_rows(const AttnParams &, const WorkItem &, int, int nvalid)
+{
+    return {nvalid, nvalid};
+}
+
+__device__ __forceinline__ TileRows tile_rows(const WinParams &, const WorkItem &w, int tpos, int nvalid)
+{
+    TileRows t;
+    t.a = min(max(w.sink_end - tpos, 0), nvalid);
+    t.b = min(max(w.dead_end - tpos, t.a), nvalid);
+    return t;
+}
 
 // Walks this CTA's segments in order; each role of a CTA keeps its own.  A
 // part of the range that holds only a unit's entry tiles yields no segment.
@@ -185,7 +247,8 @@ struct SegCursor {
     long long left;
     bool first;
 
-    __device__ __forceinline__ void init(const AttnParams &p, const CtaRange &r)
+    template <class P>
+    __device__ __forceinline__ void init(const P &p, const CtaRange &r)
     {
         left = r.g1 - r.g0;
         first = true;
@@ -210,7 +273,8 @@ struct SegCursor {
         off = rem;
     }
 
-    __device__ __forceinline__ bool next(const AttnParams &p, WorkItem &w)
+    template <class P>
+    __device__ __forceinline__ bool next(const P &p, WorkItem &w)
     {
         while (left > 0) {
             const int wu = unit_work(p, len, b);
@@ -227,6 +291,7 @@ struct SegCursor {
                 w.fin = t0 == 0 && t1 == wu - p.VT;
                 w.slot = w.fin ? -1 : 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1);
                 first = false;
+                set_window(p, w);
             }
             left -= n;
             off += n;

@@ -141,8 +141,8 @@ struct TilePages {
     int id;
 };
 
-__device__ __forceinline__ TilePages tile_pages(const AttnParams &p, const int32_t *trow, int tpos,
-                                                int nvalid, int lane)
+__device__ __forceinline__ TilePages tile_pages(const AttnParams &p, const WorkItem &,
+                                                const int32_t *trow, int tpos, int nvalid, int lane)
 {
     TilePages t;
     t.lp0 = tpos / p.P;
@@ -151,6 +151,88 @@ __device__ __forceinline__ TilePages tile_pages(const AttnParams &p, const int32
     const bool mine = (int64_t)lane * p.P < (int64_t)t.off0 + nvalid;
     t.id = mine ? __ldg(trow + t.lp0 + lane) : 0;
     return t;
+}
+
+// Under a sliding window a tile's rows are two runs, [0, rows.a) before the
+// skipped positions and [rows.b, nvalid) after them; lane l holds the id of
+// the l-th page of the first run's pages, then the second's.
+struct WinTilePages {
+    TileRows rows;
+    int lp[2], off[2];  // first page of each run, entered at slot off
+    int n_a;            // pages of the first run
+    int id;
+};
+
+__device__ __forceinline__ WinTilePages tile_pages(const WinParams &p, const WorkItem &it,
+                                                   const int32_t *trow, int tpos, int nvalid,
+                                                   int lane)
+{
+    WinTilePages t;
+    t.rows = tile_rows(p, it, tpos, nvalid);
+    const int pos_b = tpos + t.rows.b + it.skip;
+    t.lp[0] = tpos / p.P;
+    t.off[0] = tpos - t.lp[0] * p.P;
+    t.lp[1] = pos_b / p.P;
+    t.off[1] = pos_b - t.lp[1] * p.P;
+    t.n_a = t.rows.a > 0 ? (t.off[0] + t.rows.a - 1) / p.P + 1 : 0;
+    const int n_b = nvalid > t.rows.b ? (t.off[1] + nvalid - t.rows.b - 1) / p.P + 1 : 0;
+    t.id = lane < t.n_a         ? __ldg(trow + t.lp[0] + lane)
+           : lane < t.n_a + n_b ? __ldg(trow + t.lp[1] + lane - t.n_a)
+                                : 0;
+    return t;
+}
+
+// One piece (lane 0): rows [r, r + n) of ring unit st, dims [128 kb, 128 kb +
+// 128), from page `page` at slot `off`, one box per set bit of n.
+template <class Sm>
+__device__ __forceinline__ void put_piece(const AttnParams &p, Sm &sm, int st, const CUtensorMap *maps,
+                                          int page, int kh, int off, int r, int n, int kb, uint64_t pol)
+{
+    if (page < 0 || page >= p.n_pages) {
+        // never read: page 0 stands in (the stream's outputs are flagged)
+        set_flag(p.flags, kDevBadPage);
+        page = 0;
+    }
+    int row = r, y = (page * p.Hkv + kh) * p.P + off;
+    for (int m = n; m != 0;) {
+        const int h = 31 - __clz(m);  // the largest box that fits: 2^h rows
+        tma_load_2d(sm.ring[st] + row * 128, &maps[h], 128 * kb, y, &sm.full[st], pol);
+        tma_load_2d(sm.ring[st] + kRingBox + row * 128, &maps[h], 128 * kb + 64, y, &sm.full[st], pol);
+        row += 1 << h;
+        y += 1 << h;
+        m -= 1 << h;
+    }
+}
+
+template <class Sm>
+__device__ __forceinline__ bool pieces_unit(const AttnParams &p, Sm &sm, int st, uint32_t parity,
+                                            const CUtensorMap *maps, const WinTilePages &tp,
+                                            const int32_t *trow, int kh, int nvalid, int kb,
+                                            int lane, uint64_t pol)
+{
+    bool ok = true;
+    if (lane == 0) {
+        ok = pwait(sm, &sm.empty[st], parity, p.flags, kWaitEmpty);
+        if (ok)
+            mbar_arrive_expect_tx(&sm.full[st], (uint32_t)(tp.rows.a + nvalid - tp.rows.b) * 256u);
+    }
+    if (!__shfl_sync(0xffffffffu, ok, 0))
+        return false;
+    int l = 0;  // pages walked
+#pragma unroll
+    for (int run = 0; run < 2; ++run) {
+        const int r1 = run == 0 ? tp.rows.a : nvalid;
+        int off = tp.off[run], j = 0;
+        for (int r = run == 0 ? 0 : tp.rows.b; r < r1; ++j, ++l) {
+            const int n = min(r1 - r, p.P - off);
+            const int page = l < 32 ? __shfl_sync(0xffffffffu, tp.id, l) : __ldg(trow + tp.lp[run] + j);
+            if (lane == 0)
+                put_piece(p, sm, st, maps, page, kh, off, r, n, kb, pol);
+            r += n;
+            off = 0;
+        }
+    }
+    return true;
 }
 
 // The whole warp (lane 0 issues): waits until slot st is free, then loads
@@ -175,24 +257,9 @@ __device__ __forceinline__ bool pieces_unit(const AttnParams &p, Sm &sm, int st,
     int off = tp.off0;
     for (int r = 0, j = 0; r < nvalid; ++j) {
         const int n = min(nvalid - r, p.P - off);
-        int page = j < 32 ? __shfl_sync(0xffffffffu, tp.id, j) : __ldg(trow + tp.lp0 + j);
-        if (lane == 0) {
-            if (page < 0 || page >= p.n_pages) {
-                // never read: page 0 stands in (the stream's outputs are flagged)
-                set_flag(p.flags, kDevBadPage);
-                page = 0;
-            }
-            int row = r, y = (page * p.Hkv + kh) * p.P + off;
-            for (int m = n; m != 0;) {
-                const int h = 31 - __clz(m);  // the largest box that fits: 2^h rows
-                tma_load_2d(sm.ring[st] + row * 128, &maps[h], 128 * kb, y, &sm.full[st], pol);
-                tma_load_2d(sm.ring[st] + kRingBox + row * 128, &maps[h], 128 * kb + 64, y,
-                            &sm.full[st], pol);
-                row += 1 << h;
-                y += 1 << h;
-                m -= 1 << h;
-            }
-        }
+        const int page = j < 32 ? __shfl_sync(0xffffffffu, tp.id, j) : __ldg(trow + tp.lp0 + j);
+        if (lane == 0)
+            put_piece(p, sm, st, maps, page, kh, off, r, n, kb, pol);
         r += n;
         off = 0;
     }
@@ -201,8 +268,8 @@ __device__ __forceinline__ bool pieces_unit(const AttnParams &p, Sm &sm, int st,
 
 // The whole producer warp: the unit order of ring_producer, assembled from
 // pieces.  kmaps / vmaps: kBoxHeights tensor maps each.
-template <int DB, int NU, class Sm>
-__device__ __forceinline__ void ring_producer_pieces(const AttnParams &p, const CUtensorMap *kmaps,
+template <int DB, int NU, class P, class Sm>
+__device__ __forceinline__ void ring_producer_pieces(const P &p, const CUtensorMap *kmaps,
                                                      const CUtensorMap *vmaps, Sm &sm, int lane)
 {
     const uint64_t pol = l2_evict_first_policy();
@@ -211,7 +278,7 @@ __device__ __forceinline__ void ring_producer_pieces(const AttnParams &p, const 
     WorkItem it;
     uint32_t U = 0;  // units issued
     bool ok = true;
-    auto put_tile = [&](const CUtensorMap *maps, const TilePages &tp, const int32_t *trow, int kh,
+    auto put_tile = [&](const CUtensorMap *maps, const auto &tp, const int32_t *trow, int kh,
                         int nvalid) {
 #pragma unroll 1
         for (int kb = 0; ok && kb < DB; ++kb) {
@@ -227,12 +294,12 @@ __device__ __forceinline__ void ring_producer_pieces(const AttnParams &p, const 
         // rows and page ids of tiles t, t + 1 and t + 2 (the page ids are read
         // two tiles before their first use)
         auto nvalid = [&](int t) { return min(PT, it.len - (it.key0 + t * PT)); };
-        TilePages t0 = tile_pages(p, trow, it.key0, nvalid(0), lane);
-        TilePages t1 = n > 1 ? tile_pages(p, trow, it.key0 + PT, nvalid(1), lane) : t0;
+        auto t0 = tile_pages(p, it, trow, it.key0, nvalid(0), lane);
+        auto t1 = n > 1 ? tile_pages(p, it, trow, it.key0 + PT, nvalid(1), lane) : t0;
         put_tile(kmaps, t0, trow, it.kh, nvalid(0));
         for (int t = 0; ok && t < n; ++t) {
             const int pos = it.key0 + t * PT;
-            const TilePages t2 = t + 2 < n ? tile_pages(p, trow, pos + 2 * PT, nvalid(t + 2), lane) : t1;
+            const auto t2 = t + 2 < n ? tile_pages(p, it, trow, pos + 2 * PT, nvalid(t + 2), lane) : t1;
             if (t + 1 < n)
                 put_tile(kmaps, t1, trow, it.kh, nvalid(t + 1));
             if (ok)
@@ -250,6 +317,25 @@ __device__ __forceinline__ void ring_producer_pieces(const AttnParams &p, const 
         }
     }
     __syncwarp();
+}
+
+// Two probabilities as bf16 pairs hi and lo with p = hi + lo: both truncated
+// (|p - hi - lo| < 2^-14 p), or under kRn both rounded to nearest (at most
+// 2^-18 p, without a bias), at the same number of instructions.
+template <bool kRn>
+__device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo)
+{
+    if constexpr (kRn) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
+        const float r0 = p0 - bf_lo(hi), r1 = p1 - bf_hi(hi);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(r1), "f"(r0));
+    } else {
+        const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+        hi = __byte_perm(b0, b1, 0x7632);
+        const float r0 = p0 - __uint_as_float(b0 & 0xffff0000u);
+        const float r1 = p1 - __uint_as_float(b1 & 0xffff0000u);
+        lo = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
+    }
 }
 
 // Ring index of the first V unit of tile t of a segment that starts at the

@@ -87,15 +87,21 @@ constexpr int kEntrySimt = 0;
 // max_len on (measured crossover near 5,700 positions).
 constexpr int kPmDecodeMinLen = 6144;
 
+// A sliding-window call's host arguments (window 0: a plain call).
+struct Window {
+    int32_t window = 0;
+    int32_t sinks = 0;
+};
+
 struct Plan {
-    AttnParams p;
+    WinParams p;  // a plain call launches its AttnParams part
     int grid;
     size_t ws_bytes;
     Kernel kernel;  // which partial kernel runs the call
 };
 
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
-              int32_t rows_max, bool tree, Plan *plan)
+              int32_t rows_max, bool tree, Plan *plan, const Window *win = nullptr)
 {
     int rc = check_pool_streams(pool, st);
     if (rc != TF_OK)
@@ -108,13 +114,20 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     const int64_t M = (int64_t)G * rows;
     if (M > (1 << 20))
         return TF_EINVAL;
+    if (win && (win->window < 1 || win->sinks < 0))
+        return TF_EINVAL;
     int sms = 0;
     rc = device_sm_count(&sms);
     if (rc != TF_OK)
         return rc;
 
-    AttnParams &p = plan->p;
-    p = AttnParams{};
+    WinParams &p = plan->p;
+    p = WinParams{};
+    if (win) {
+        // a window or sinks past every length see what max_len does
+        p.window = win->window < st->max_len ? win->window : st->max_len;
+        p.sinks = win->sinks < st->max_len ? win->sinks : st->max_len;
+    }
     p.n_pages = pool->n_pages;
     p.Hkv = pool->n_kv_heads;
     p.P = pool->page_size;
@@ -160,7 +173,20 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     const bool long_context = st->max_len >= kPmDecodeMinLen;
     plan->kernel = Kernel::kSimt;
     p.RB = kSimtRows;
-    if (tree) {
+    if (win) {
+        // a sliding window: the tensor-core kernels (any row count and page
+        // size); pools past 2^31 rows are refused
+        const int nr = pm_rows(p);
+        if (nr > 0) {
+            plan->kernel = Kernel::kPm;
+            p.RB = nr;
+        } else if (prompt_supported(p)) {
+            plan->kernel = Kernel::kPrompt;
+            p.RB = prompt_rows();
+        } else {
+            return TF_EUNSUPPORTED;
+        }
+    } else if (tree) {
         // tree masks: the position-major kernel (any row count), else the
         // CUDA-core kernel (pools past 2^31 rows)
         const int nr = pm_rows(p);
@@ -196,7 +222,9 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
          : plan->kernel == Kernel::kPrompt ? kEntryPrompt : kEntrySimt;
     // One persistent CTA per SM, but no more than the work the call can have
     // with every stream at max_len (the device splits the actual work).
-    const int64_t tiles_max = (int64_t)p.S * p.Hkv * head_work(p, st->max_len);
+    const int64_t head_max = win ? head_work(p, st->max_len)
+                                 : head_work(static_cast<const AttnParams &>(p), st->max_len);
+    const int64_t tiles_max = (int64_t)p.S * p.Hkv * head_max;
     int64_t grid = sms < kMaxCtas ? sms : kMaxCtas;
     if (tiles_max < grid)
         grid = tiles_max > 0 ? tiles_max : 1;
@@ -220,12 +248,30 @@ struct Faults {
     int32_t withhold = 0;
 };
 
+template <class P>
+cudaError_t launch_merge(const P &p, cudaStream_t s)
+{
+    return p.D == 128   ? launch_attn_merge<128>(p, s)
+           : p.D == 256 ? launch_attn_merge<256>(p, s)
+                        : launch_attn_merge<512>(p, s);
+}
+
+// The partial kernel and the merge of a call on the tensor-core kernels.
+template <class P>
+cudaError_t launch_tensor_core(const P &p, const Plan &plan, cudaStream_t s)
+{
+    cudaError_t e = plan.kernel == Kernel::kPm ? launch_attn_pm(p, plan.grid, s)
+                                               : launch_attn_prompt(p, plan.grid, s);
+    return e == cudaSuccess ? launch_merge(p, s) : e;
+}
+
 int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32_t Hq,
               int32_t rows, int32_t rows_max, const uint8_t *tree, float scale, float *out,
-              void *ws, size_t ws_bytes, void *stream, const Faults &faults = Faults{})
+              void *ws, size_t ws_bytes, void *stream, const Faults &faults = Faults{},
+              const Window *win = nullptr)
 {
     Plan plan;
-    int rc = make_plan(pool, st, Hq, rows, rows_max, tree != nullptr, &plan);
+    int rc = make_plan(pool, st, Hq, rows, rows_max, tree != nullptr, &plan, win);
     if (rc != TF_OK)
         return rc;
     plan.p.wait_limit = faults.wait_limit;
@@ -254,16 +300,10 @@ int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (plan.kernel == Kernel::kPm) {
-        e = launch_attn_pm(p, plan.grid, s);
-        if (e == cudaSuccess)
-            e = p.D == 128   ? launch_attn_merge<128>(p, s)
-                : p.D == 256 ? launch_attn_merge<256>(p, s)
-                             : launch_attn_merge<512>(p, s);
-    } else if (plan.kernel == Kernel::kPrompt) {
-        e = launch_attn_prompt(p, plan.grid, s);
-        if (e == cudaSuccess)
-            e = launch_attn_merge<128>(p, s);
+    if (win) {
+        e = launch_tensor_core(plan.p, plan, s);
+    } else if (plan.kernel != Kernel::kSimt) {
+        e = launch_tensor_core(p, plan, s);
     } else if (p.D == 128) {
         e = launch_attn_simt<128>(p, plan.grid, s);
         if (e == cudaSuccess)
@@ -408,6 +448,46 @@ int tf_paged_attn_prompt(const tf_kv_pool *pool, const tf_streams *streams, cons
 {
     return attn_call(pool, streams, q, n_q_heads, rows, 4096, nullptr, scale, out, workspace,
                      workspace_bytes, stream);
+}
+
+size_t tf_paged_attn_window_workspace_bytes(const tf_kv_pool *pool, const tf_streams *streams,
+                                            int32_t n_q_heads, int32_t rows, int32_t window,
+                                            int32_t sinks)
+{
+    const Window win{window, sinks};
+    Plan plan;
+    if (make_plan(pool, streams, n_q_heads, rows, 4096, false, &plan, &win) != TF_OK)
+        return 0;
+    return plan.ws_bytes;
+}
+
+int tf_paged_attn_decode_window(const tf_kv_pool *pool, const tf_streams *streams, const void *q,
+                                int32_t n_q_heads, int32_t window, int32_t sinks, float scale,
+                                float *out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const Window win{window, sinks};
+    return attn_call(pool, streams, q, n_q_heads, 1, 1, nullptr, scale, out, workspace,
+                     workspace_bytes, stream, Faults{}, &win);
+}
+
+int tf_paged_attn_verify_window(const tf_kv_pool *pool, const tf_streams *streams, const void *q,
+                                int32_t n_q_heads, int32_t rows, int32_t window, int32_t sinks,
+                                float scale, float *out, void *workspace, size_t workspace_bytes,
+                                void *stream)
+{
+    const Window win{window, sinks};
+    return attn_call(pool, streams, q, n_q_heads, rows, 8, nullptr, scale, out, workspace,
+                     workspace_bytes, stream, Faults{}, &win);
+}
+
+int tf_paged_attn_prompt_window(const tf_kv_pool *pool, const tf_streams *streams, const void *q,
+                                int32_t n_q_heads, int32_t rows, int32_t window, int32_t sinks,
+                                float scale, float *out, void *workspace, size_t workspace_bytes,
+                                void *stream)
+{
+    const Window win{window, sinks};
+    return attn_call(pool, streams, q, n_q_heads, rows, 4096, nullptr, scale, out, workspace,
+                     workspace_bytes, stream, Faults{}, &win);
 }
 
 int tf_testing_paged_attn(const tf_kv_pool *pool, const tf_streams *streams, const void *q,

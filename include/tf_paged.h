@@ -87,6 +87,7 @@ extern "C" {
 #define TF_DEV_BAD_LEN 1u   /* some lens[s] outside [rows, min(max_len, table_stride*page_size)] */
 #define TF_DEV_BAD_PAGE 2u  /* some table entry in use outside [0, n_pages) */
 #define TF_DEV_TIMEOUT 4u   /* a pipeline wait gave up (an internal error) */
+#define TF_DEV_NO_PAGE 8u   /* tf_kv_pages_grow: too few free pages (nothing was changed) */
 
 /* The pool: K and V pages, device memory, 16-byte aligned.
  * page_size may be any positive size at every head dim (TensorFold #1620,
@@ -125,6 +126,48 @@ TF_API int tf_kv_put_rows(const tf_kv_pool *pool, const tf_streams *streams,
                    const void *k_rows, const void *v_rows, int32_t rows,
                    void *stream);
 
+/* Rotary positions of a layer.  Pair i (0 <= i < rotary_dim / 2) of a head is
+ * dims (i, i + rotary_dim / 2), or with `adjacent` dims (2i, 2i + 1); it is
+ * turned by the angle position[axis] * inv_freq[i], where axis =
+ * pair_axis[i].  Dims from rotary_dim on are kept.  One axis is the rotary
+ * position of text; images and video give each token a time, a height and a
+ * width, and pair_axis says which pairs each of them turns (contiguous
+ * sections or interleaved: any assignment). */
+typedef struct tf_rope {
+    const float *inv_freq;     /* device, [rotary_dim / 2] */
+    const uint8_t *pair_axis;  /* host, [rotary_dim / 2], each < n_axes; NULL: all axis 0 */
+    int32_t rotary_dim;        /* even, in [2, head_dim] */
+    int32_t n_axes;            /* in [1, 4] */
+    int32_t adjacent;          /* 0 or 1 */
+} tf_rope;
+
+/* Row write with rotary positions: turns a step's query and key rows and
+ * writes keys and values into their pages, in one pass over the rows
+ * (tf_kv_put_rows is the write alone).
+ *  positions  device int32 [n_streams][rows][n_axes]: the rows' rotary
+ *             positions, of either sign; the slot a row is written to
+ *             follows lens, as in tf_kv_put_rows
+ *  q          bf16, n_streams * rows rows of n_q_heads * head_dim values,
+ *             q_stride elements from one to the next; q_out receives the
+ *             turned rows, [n_streams][rows][n_q_heads][head_dim].  q_out may
+ *             be q (with q_stride = n_q_heads * head_dim); the two must not
+ *             overlap otherwise.  n_q_heads = 0: no queries (q and q_out may
+ *             be null)
+ *  k_rows, v_rows  likewise with n_kv_heads heads and strides of their own, so
+ *             that q, k and v may be slices of one projection's output
+ * Pointers are 16-byte aligned and strides are multiples of 8 elements, at
+ * least the row's size.  Angles are formed in 64 bits, turned values in fp32
+ * and rounded once; values and kept dims are copied bit for bit.  K/V rows
+ * whose stream length or page id is out of range are skipped (their queries
+ * are turned all the same); nothing else of the pool is touched.
+ * Returns TF_OK, TF_EINVAL, TF_EUNSUPPORTED (head_dim) or TF_ECUDA. */
+TF_API int tf_kv_put_rows_rope(const tf_kv_pool *pool, const tf_streams *streams,
+                               const tf_rope *rope, const int32_t *positions,
+                               const void *q, int64_t q_stride, void *q_out,
+                               int32_t n_q_heads, const void *k_rows, int64_t k_stride,
+                               const void *v_rows, int64_t v_stride, int32_t rows,
+                               void *stream);
+
 /* The state copy (TensorFold #1620, opening comment, "Kept states" bullet:
  * a kept state is copied by walking the slot's pages).  For every stream s
  * and position j < src->lens[s], the head_dim bf16 values of K and of V of
@@ -148,6 +191,110 @@ TF_API int tf_kv_put_rows(const tf_kv_pool *pool, const tf_streams *streams,
 TF_API int tf_kv_copy_state(const tf_kv_pool *src_pool, const tf_streams *src,
                             const tf_kv_pool *dst_pool, const int32_t *dst_table,
                             int32_t dst_table_stride, uint32_t *status, void *stream);
+
+/* Shared pages (TensorFold #1620, opening comment: a stream takes pages of
+ * the core pool as it grows; the host leases them there).  The pool's
+ * bookkeeping is one device array, refs[page]: how many table entries hold the
+ * page, 0 for a free one.  A table entry that holds no page is -1.  A cache
+ * starts with refs all 0 and its table all -1.  All calls are enqueued on
+ * `stream`, keep no state elsewhere, and give results that depend on refs, the
+ * tables and lens alone (pages are taken lowest id first), so they may be
+ * captured and replayed.  Calls on the same refs must be ordered by the
+ * caller.
+ *  refs  device int32 [n_pages], 16-byte aligned
+ * Every call takes an optional status word (device uint32, 4-byte aligned)
+ * into which TF_DEV_* bits are ORed. */
+typedef struct tf_kv_pages {
+    int32_t *refs;
+    int32_t n_pages;
+    int32_t page_size;
+} tf_kv_pages;
+
+/* Fork: child row c of dst_table names the pages that hold the positions
+ * [0, src_lens[parents[c]]) of its parent's row, one holder more each
+ * (entries of -1, behind a sliding window, stay -1), the rest of the row is
+ * -1, and dst_lens[c] is the parent's length.  parents[c] = -1 makes an empty
+ * child.  One parent may have any number of children: n beams, n samples of a
+ * prompt.  A reordering of beams forks into a second table and frees the
+ * first.
+ *  dst rows  are overwritten, not released: they hold no pages before the
+ *            call.  They may be rows of src_table's memory that are no
+ *            parent's; dst_lens must not overlap src_lens.
+ * A parent outside [-1, n_src) or whose pages exceed either table's row makes
+ * an empty child and sets TF_DEV_BAD_LEN; a page outside the pool, or one
+ * that nobody holds, is left out (-1) and sets TF_DEV_BAD_PAGE. */
+TF_API int tf_kv_pages_fork(const tf_kv_pages *pages, const int32_t *src_table,
+                            int32_t src_stride, const int32_t *src_lens, int32_t n_src,
+                            const int32_t *parents, int32_t n_dst, int32_t *dst_table,
+                            int32_t dst_stride, int32_t *dst_lens, uint32_t *status,
+                            void *stream);
+
+/* Free: entries [first[s], end[s]) of row s give their pages back (one holder
+ * fewer; at 0 the page is free) and hold -1.  first null: from entry 0; end
+ * null: to the row's end (both null: the streams are dropped).  Rolling back
+ * drafts frees the entries past the last one in use.  Entries of -1 are
+ * passed over.  A range outside the row frees nothing of it (TF_DEV_BAD_LEN);
+ * a page that is outside the pool, or that nobody holds, sets
+ * TF_DEV_BAD_PAGE. */
+TF_API int tf_kv_pages_free(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                            int32_t n_streams, const int32_t *first, const int32_t *end,
+                            uint32_t *status, void *stream);
+
+/* Frees the pages that a sliding window has left behind: those whose
+ * positions are all at or past `sinks` and at or before lens[s] - window, so
+ * that no row at position lens[s] or later sees any of them (rows already in
+ * the cache might: call it after the step's attention).  window >= 1,
+ * sinks >= 0. */
+TF_API int tf_kv_pages_free_window(const tf_kv_pages *pages, int32_t *table,
+                                   int32_t table_stride, const int32_t *lens,
+                                   int32_t n_streams, int32_t window, int32_t sinks,
+                                   uint32_t *status, void *stream);
+
+/* A list of page moves: device int32 [1 + cap][4], 16-byte aligned.  Entry 0
+ * is the head {moves, live pages (compact), 0, 0}; entry k >= 1 is {source
+ * page or -1 (nothing to copy), destination page, positions to copy, -}.
+ * tf_kv_pages_grow and _compact write it, tf_kv_pages_move performs it. */
+#define TF_MOVE_BYTES 16
+
+/* Grow: gives every position that the step's rows will be written to, lens[s]
+ * - rows .. lens[s] - 1 (lens counts them already, as everywhere), a page of
+ * the stream's own.  An entry of -1 gets a free page; an entry whose page
+ * others hold too gets one in its place (one holder fewer for the old page)
+ * and a move of the page's earlier positions (copy on write); an entry whose
+ * page is the stream's own stays.  Holders are counted at the start of the
+ * call: two streams that grow into the page they share both get their own.
+ * A stream of length 0 is passed over; a length outside [rows, table_stride *
+ * page_size] sets TF_DEV_BAD_LEN, a page outside the pool, or that nobody
+ * holds, TF_DEV_BAD_PAGE, and both are left alone.  When the free pages do
+ * not suffice for all streams the call changes nothing, the list is empty and
+ * TF_DEV_NO_PAGE is set: read the status before the rows are written.
+ *  moves, moves_bytes  the list; TF_ENOSPACE unless it can hold an entry for
+ *                      every page the rows may touch: cap >= n_streams *
+ *                      ((rows + page_size - 2) / page_size + 1)
+ * The moves are performed (on every layer's pool) before rows are written and
+ * before the next call that changes refs. */
+TF_API int tf_kv_pages_grow(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                            const int32_t *lens, int32_t n_streams, int32_t rows,
+                            void *moves, size_t moves_bytes, uint32_t *status, void *stream);
+
+/* Compact: moves the live pages to ids 0 .. n_live - 1 (the k-th live page at
+ * or past n_live, in ascending order, to the k-th free one below it), and
+ * makes refs and the table's entries follow.  The list's head holds the
+ * number of moves and n_live, so that a caller may give the pool's tail back.
+ * Every table that holds pages must be the one passed: entries elsewhere go
+ * stale.
+ *  moves  cap >= n_pages / 2, else TF_ENOSPACE */
+TF_API int tf_kv_pages_compact(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                               int32_t n_streams, void *moves, size_t moves_bytes,
+                               uint32_t *status, void *stream);
+
+/* Performs a list's moves on one layer's pool: for every entry the first
+ * `positions` positions of the source page, K and V of every KV head, are
+ * copied bit for bit to the destination page.  Entries without a source are
+ * passed over, ones outside the pool set TF_DEV_BAD_PAGE.  The list stays as
+ * it is. */
+TF_API int tf_kv_pages_move(const tf_kv_pool *pool, const void *moves, size_t moves_bytes,
+                            uint32_t *status, void *stream);
 
 /* Workspace bytes an attention call with these arguments needs on the
  * current device (0 on a bad argument).  Follows the scratch convention of

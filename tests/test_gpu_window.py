@@ -163,6 +163,18 @@ def test_lengths_out_of_range_and_bad_pages_are_reported():
     assert tf.tf_workspace_status(ws) & tf.TF_DEV_BAD_PAGE
 
 
+def test_refusals_that_need_the_device():
+    import verify_paged_gqa_b200 as tf
+    c = WindowCase([900, 1500], 1, 200, 4, P=64, seed=9)
+    out, ws = torch.zeros(c.q.shape, dtype=torch.float32, device="cuda"), c.workspace()
+    call = lambda scale, ws: tf.tf_paged_attn_decode_window(c.k_pool, c.v_pool, c.table, c.lens, c.q, 200, 4, scale, out, ws, 1500)  # noqa: E731
+    for scale, w, want in ((float("nan"), ws, tf.TF_EINVAL), (float("inf"), ws, tf.TF_EINVAL), (0.1, ws[:-16], tf.TF_ENOSPACE)):
+        with pytest.raises(tf.TFError) as e:
+            call(scale, w)
+        assert e.value.status == want
+    assert not out.any()
+
+
 def test_a_captured_call_follows_the_lengths():
     import verify_paged_gqa_b200 as tf
     c = WindowCase([1500, 1200, 700], 1, 400, 4, P=64, seed=11)

@@ -37,7 +37,8 @@ def _header_value(name: str) -> int:
         if m:
             return int(m.group(1))
     return {"TF_OK": 0, "TF_EINVAL": 1, "TF_EUNSUPPORTED": 2, "TF_ENOSPACE": 3,
-            "TF_ECUDA": 4, "TF_DEV_BAD_LEN": 1, "TF_DEV_BAD_PAGE": 2, "TF_DEV_TIMEOUT": 4}[name]
+            "TF_ECUDA": 4, "TF_DEV_BAD_LEN": 1, "TF_DEV_BAD_PAGE": 2, "TF_DEV_TIMEOUT": 4,
+            "TF_DEV_NO_PAGE": 8, "TF_MOVE_BYTES": 16}[name]
 
 
 TF_OK = _header_value("TF_OK")
@@ -48,6 +49,8 @@ TF_ECUDA = _header_value("TF_ECUDA")
 TF_DEV_BAD_LEN = _header_value("TF_DEV_BAD_LEN")
 TF_DEV_BAD_PAGE = _header_value("TF_DEV_BAD_PAGE")
 TF_DEV_TIMEOUT = _header_value("TF_DEV_TIMEOUT")
+TF_DEV_NO_PAGE = _header_value("TF_DEV_NO_PAGE")
+TF_MOVE_BYTES = _header_value("TF_MOVE_BYTES")
 
 if not os.path.exists(library_path):
     raise ImportError(
@@ -65,6 +68,17 @@ class tf_streams(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int32),
                 ("lens", ctypes.c_void_p), ("n_streams", ctypes.c_int32),
                 ("max_len", ctypes.c_int32)]
+
+
+class tf_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32)]
+
+
+class tf_kv_pages(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
 
 
 raw = ctypes.CDLL(library_path)
@@ -97,6 +111,19 @@ for _name in ("tf_paged_attn_verify_window", "tf_paged_attn_prompt_window"):
 raw.tf_kv_copy_state.argtypes = [_P(tf_kv_pool), _P(tf_streams), _P(tf_kv_pool), _vp, _i32, _vp,
                                  _vp]
 raw.tf_kv_copy_state.restype = ctypes.c_int
+_i64 = ctypes.c_int64
+raw.tf_kv_put_rows_rope.argtypes = [_P(tf_kv_pool), _P(tf_streams), _P(tf_rope), _vp, _vp, _i64,
+                                    _vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp]
+raw.tf_kv_put_rows_rope.restype = ctypes.c_int
+raw.tf_kv_pages_fork.argtypes = [_P(tf_kv_pages), _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp,
+                                 _vp, _vp]
+raw.tf_kv_pages_free.argtypes = [_P(tf_kv_pages), _vp, _i32, _i32, _vp, _vp, _vp, _vp]
+raw.tf_kv_pages_free_window.argtypes = [_P(tf_kv_pages), _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp]
+raw.tf_kv_pages_grow.argtypes = [_P(tf_kv_pages), _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp, _vp]
+raw.tf_kv_pages_compact.argtypes = [_P(tf_kv_pages), _vp, _i32, _i32, _vp, _sz, _vp, _vp]
+raw.tf_kv_pages_move.argtypes = [_P(tf_kv_pool), _vp, _sz, _vp, _vp]
+for _name in ("fork", "free", "free_window", "grow", "compact", "move"):
+    getattr(raw, f"tf_kv_pages_{_name}").restype = ctypes.c_int
 raw.tf_testing_paged_attn.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _i32, _i32, _f32,
                                       _vp, _vp, _sz, ctypes.c_int64, _i32, _vp]
 raw.tf_testing_paged_attn.restype = ctypes.c_int
@@ -161,6 +188,176 @@ def tf_kv_put_rows(k_pool, v_pool, table, lens, k_rows, v_rows, max_len, stream=
     _check(raw.tf_kv_put_rows(ctypes.byref(pool), ctypes.byref(st), k_rows.data_ptr(),
                               v_rows.data_ptr(), k_rows.shape[1], _stream(stream)),
            "tf_kv_put_rows")
+
+
+class Rope:
+    """A layer's rotary positions (``tf_rope`` in the header), kept for its calls.
+
+    inv_freq   float32 device tensor [rotary_dim / 2]
+    pair_axis  the axis of each pair (a sequence of rotary_dim / 2 numbers
+               below n_axes); None: every pair turns by axis 0
+    adjacent   pair i is dims (2i, 2i + 1) instead of (i, i + rotary_dim / 2)
+    """
+
+    def __init__(self, inv_freq, pair_axis=None, n_axes=1, adjacent=False):
+        _need(inv_freq, torch.float32, 1, "inv_freq")
+        pairs = inv_freq.shape[0]
+        self.inv_freq, self.n_axes = inv_freq, int(n_axes)
+        self._axes = None
+        if pair_axis is not None:
+            axes = [int(a) for a in pair_axis]
+            if len(axes) != pairs:
+                raise ValueError("pair_axis must name an axis for each of inv_freq's pairs")
+            if any(a < 0 or a >= self.n_axes for a in axes):
+                raise ValueError("pair_axis names an axis outside [0, n_axes)")
+            self._axes = (ctypes.c_uint8 * pairs)(*axes)
+        self.struct = tf_rope(inv_freq.data_ptr(),
+                              None if self._axes is None else ctypes.addressof(self._axes),
+                              2 * pairs, self.n_axes, 1 if adjacent else 0)
+
+
+def _rows(t, heads, d, S, W, name):
+    """Pointer and row stride of step rows [S][W][heads][d] that may be slices
+    of a wider projection output: heads and dims dense, rows evenly apart."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 4:
+        raise TypeError(f"{name} must be a bfloat16 tensor with 4 dims")
+    if tuple(t.shape) != (S, W, heads, d):
+        raise ValueError(f"{name} must be [{S}][{W}][{heads}][{d}], not {list(t.shape)}")
+    st = t.stride()
+    row = st[1] if W > 1 else st[0] if S > 1 else heads * d
+    if ((d > 1 and st[3] != 1) or (heads > 1 and st[2] != d) or (W > 1 and S > 1 and st[0] != W * row)):
+        raise ValueError(f"{name}: heads and dims must be dense and rows evenly spaced")
+    return t.data_ptr(), row
+
+
+def tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, positions, rope, max_len,
+                        q_out=None, stream=None):
+    """Turns a step's rows q [S][W][Hq][d] and k_rows [S][W][Hkv][d] by their
+    rotary positions (int32 [S][W][n_axes]) and writes k_rows and v_rows into
+    their pages.  The rows may be slices of one projection's output.  Returns
+    the turned queries (q_out, a new tensor by default, or q itself to turn
+    them in place); q may be None."""
+    pool, st = _pool(k_pool, v_pool), _streams(table, lens, max_len)
+    _need(positions, torch.int32, 3, "positions")
+    if positions.shape[0] != st.n_streams or positions.shape[2] != rope.n_axes:
+        raise ValueError("positions must be [n_streams][rows][n_axes]")
+    S, W = st.n_streams, positions.shape[1]
+    hq, qp, qs, qo = 0, None, 0, None
+    if q is not None:
+        hq = q.shape[2] if q.dim() == 4 else 0
+        qp, qs = _rows(q, hq, pool.head_dim, S, W, "q")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _need(q_out, torch.bfloat16, 4, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qo = q_out.data_ptr()
+    kp, ks = _rows(k_rows, pool.n_kv_heads, pool.head_dim, S, W, "k_rows")
+    vp, vs = _rows(v_rows, pool.n_kv_heads, pool.head_dim, S, W, "v_rows")
+    _check(raw.tf_kv_put_rows_rope(ctypes.byref(pool), ctypes.byref(st), ctypes.byref(rope.struct),
+                                   positions.data_ptr(), qp, qs, qo, hq, kp, ks, vp, vs, W,
+                                   _stream(stream)), "tf_kv_put_rows_rope")
+    return q_out
+
+
+def _pages(refs, page_size):
+    _need(refs, torch.int32, 1, "refs")
+    return tf_kv_pages(refs.data_ptr(), refs.shape[0], int(page_size))
+
+
+def _row_ints(t, n, name):
+    """Pointer of an int32 tensor with one element per stream (None: null)."""
+    if t is None:
+        return None
+    _need(t, torch.int32, 1, name)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have one element per row")
+    return t.data_ptr()
+
+
+def _status(status):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise TypeError("status must be an int32 tensor")
+    return status.data_ptr()
+
+
+def _moves(moves):
+    _need(moves, torch.int32, 2, "moves")
+    if moves.shape[1] != 4:
+        raise ValueError("moves must be [1 + cap][4]")
+    return moves.data_ptr(), moves.shape[0] * TF_MOVE_BYTES
+
+
+def tf_kv_pages_fork(refs, page_size, src_table, src_lens, parents, dst_table, dst_lens,
+                     status=None, stream=None):
+    """Child row c of dst_table names the pages of src_table's row parents[c]
+    (-1: none), each with one holder more in refs; dst_lens gets the lengths.
+    status: optional int32 device tensor of one element that collects TF_DEV_*
+    bits (every tf_kv_pages_* call takes one)."""
+    pg = _pages(refs, page_size)
+    _need(src_table, torch.int32, 2, "src_table")
+    _need(dst_table, torch.int32, 2, "dst_table")
+    n_src, n_dst = src_table.shape[0], dst_table.shape[0]
+    _check(raw.tf_kv_pages_fork(ctypes.byref(pg), src_table.data_ptr(), src_table.shape[1],
+                                _row_ints(src_lens, n_src, "src_lens"), n_src,
+                                _row_ints(parents, n_dst, "parents"), n_dst, dst_table.data_ptr(),
+                                dst_table.shape[1], _row_ints(dst_lens, n_dst, "dst_lens"),
+                                _status(status), _stream(stream)), "tf_kv_pages_fork")
+
+
+def tf_kv_pages_free(refs, page_size, table, first=None, end=None, status=None, stream=None):
+    """Entries [first[s], end[s]) of the table's rows (default: all) give their
+    pages back and hold -1."""
+    pg = _pages(refs, page_size)
+    _need(table, torch.int32, 2, "table")
+    n = table.shape[0]
+    _check(raw.tf_kv_pages_free(ctypes.byref(pg), table.data_ptr(), table.shape[1], n,
+                                _row_ints(first, n, "first"), _row_ints(end, n, "end"),
+                                _status(status), _stream(stream)), "tf_kv_pages_free")
+
+
+def tf_kv_pages_free_window(refs, page_size, table, lens, window, sinks, status=None, stream=None):
+    """Frees the pages wholly behind every stream's sliding window (and past its sinks)."""
+    pg = _pages(refs, page_size)
+    _need(table, torch.int32, 2, "table")
+    n = table.shape[0]
+    _check(raw.tf_kv_pages_free_window(ctypes.byref(pg), table.data_ptr(), table.shape[1],
+                                       _row_ints(lens, n, "lens"), n, int(window), int(sinks),
+                                       _status(status), _stream(stream)),
+           "tf_kv_pages_free_window")
+
+
+def tf_kv_pages_grow(refs, page_size, table, lens, rows, moves, status=None, stream=None):
+    """Gives the last ``rows`` positions of every stream pages of their own
+    (copy on write); moves: int32 [1 + cap][4], the list for tf_kv_pages_move."""
+    pg = _pages(refs, page_size)
+    _need(table, torch.int32, 2, "table")
+    n = table.shape[0]
+    mp, mb = _moves(moves)
+    _check(raw.tf_kv_pages_grow(ctypes.byref(pg), table.data_ptr(), table.shape[1],
+                                _row_ints(lens, n, "lens"), n, int(rows), mp, mb, _status(status),
+                                _stream(stream)), "tf_kv_pages_grow")
+
+
+def tf_kv_pages_compact(refs, page_size, table, moves, status=None, stream=None):
+    """Moves the live pages to the lowest ids; refs and the table follow, moves
+    gets the list for tf_kv_pages_move (its head: the moves, the live pages)."""
+    pg = _pages(refs, page_size)
+    _need(table, torch.int32, 2, "table")
+    mp, mb = _moves(moves)
+    _check(raw.tf_kv_pages_compact(ctypes.byref(pg), table.data_ptr(), table.shape[1],
+                                   table.shape[0], mp, mb, _status(status), _stream(stream)),
+           "tf_kv_pages_compact")
+
+
+def tf_kv_pages_move(k_pool, v_pool, moves, status=None, stream=None):
+    """Performs a list's page moves on one layer's pool."""
+    pool = _pool(k_pool, v_pool)
+    mp, mb = _moves(moves)
+    _check(raw.tf_kv_pages_move(ctypes.byref(pool), mp, mb, _status(status), _stream(stream)),
+           "tf_kv_pages_move")
 
 
 def tf_kv_copy_state(src_k, src_v, src_table, lens, dst_k, dst_v, dst_table, max_len,

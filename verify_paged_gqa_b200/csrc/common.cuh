@@ -15,6 +15,7 @@ namespace tfp {
 constexpr uint32_t kDevBadLen = 1u;
 constexpr uint32_t kDevBadPage = 2u;
 constexpr uint32_t kDevTimeout = 4u;
+constexpr uint32_t kDevNoPage = 8u;
 
 // The workspace starts with a 256-byte header; word 0 is the status word.
 constexpr size_t kWsHeaderBytes = 256;

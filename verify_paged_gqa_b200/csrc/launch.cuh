@@ -61,6 +61,27 @@ struct PutParams {
 
 cudaError_t launch_kv_put(const PutParams &p, cudaStream_t stream);
 
+// The row write with rotary positions (kv_rope.cu).
+struct RopeParams {
+    __nv_bfloat16 *k_pool;
+    __nv_bfloat16 *v_pool;
+    const int32_t *table;
+    const int32_t *lens;
+    const __nv_bfloat16 *q;       // rows of Hq heads, q_stride elements apart
+    const __nv_bfloat16 *k;
+    const __nv_bfloat16 *v;
+    __nv_bfloat16 *q_out;         // [S][W][Hq][D]
+    const int32_t *positions;     // [S][W][n_axes]
+    const float *inv_freq;        // [rotary / 2]
+    int64_t q_stride, k_stride, v_stride;
+    int32_t n_pages, Hkv, Hq, P, D;
+    int32_t table_stride, S, W, max_len;
+    int32_t rotary, n_axes, adjacent;
+    uint8_t pair_axis[256];       // axis of pair i
+};
+
+cudaError_t launch_kv_rope(const RopeParams &p, cudaStream_t stream);
+
 // The state copy (kv_copy.cu): positions [0, lens[s]) of every KV head from
 // the source pool's pages to the destination pool's pages.
 struct CopyParams {
@@ -80,6 +101,43 @@ struct CopyParams {
 
 int copy_chunk_positions(int head_dim);
 cudaError_t launch_kv_copy(const CopyParams &p, cudaStream_t stream);
+
+// The pages' bookkeeping (kv_pages.cu); each call uses what it needs.
+struct PagesParams {
+    int32_t *refs;              // table entries that hold each page; 16-byte aligned
+    int32_t n_pages, P;
+    int32_t *table;             // [S][stride], -1: no page
+    const int32_t *lens;
+    int32_t stride, S;
+    uint32_t *status;           // TF_DEV_* bits are ORed in (may be null)
+    // fork
+    const int32_t *parents;
+    int32_t *dst_table, *dst_lens;
+    int32_t dst_stride;
+    // free
+    const int32_t *first, *end;  // may be null: from the first, to the last entry
+    int32_t window, sinks;
+    // grow and compact: the list of page moves, entry 0 its head
+    int4 *moves;
+    int32_t rows, per_stream;    // grow: new positions, and the pages they can touch
+};
+
+cudaError_t launch_pages_fork(const PagesParams &p, int n_dst, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesParams &p, bool window, cudaStream_t stream);
+cudaError_t launch_pages_grow(const PagesParams &p, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams &p, cudaStream_t stream);
+
+struct MoveParams {
+    void *k_pool;
+    void *v_pool;
+    const int32_t *moves;
+    uint32_t *status;
+    int32_t n_pages, Hkv, P, D;
+    int32_t cap;                 // entries the list can hold
+    int32_t pieces, per_head;    // (set by the launcher) runs per page and KV head
+};
+
+cudaError_t launch_pages_move(MoveParams p, int sms, cudaStream_t stream);
 
 // Rows per row block of the CUDA-core partial kernel.
 constexpr int kSimtRows = 4;

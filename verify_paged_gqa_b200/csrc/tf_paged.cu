@@ -116,11 +116,6 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         return TF_EINVAL;
     if (win && (win->window < 1 || win->sinks < 0))
         return TF_EINVAL;
-    int sms = 0;
-    rc = device_sm_count(&sms);
-    if (rc != TF_OK)
-        return rc;
-
     WinParams &p = plan->p;
     p = WinParams{};
     if (win) {
@@ -213,6 +208,10 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
             p.RB = prompt_rows();
         }
     }
+    int sms = 0;
+    rc = device_sm_count(&sms);
+    if (rc != TF_OK)
+        return rc;
     p.n_rblk = static_cast<int32_t>((M + p.RB - 1) / p.RB);
     p.SR = static_cast<int32_t>(M < p.RB ? M : p.RB);
 
@@ -316,6 +315,39 @@ int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32
     return e == cudaSuccess ? TF_OK : TF_ECUDA;
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The checks every page call shares; fills the common parameters.
+int check_pages(const tf_kv_pages *pages, int32_t *table, int32_t stride, int32_t n_streams,
+                uint32_t *status, PagesParams *p)
+{
+    if (!pages || pages->n_pages < 1 || pages->page_size < 1 || !pages->refs ||
+        !aligned16(pages->refs) || !aligned4(status))
+        return TF_EINVAL;
+    if (n_streams < 0 || stride < 1 || (int64_t)n_streams * stride > INT32_MAX)
+        return TF_EINVAL;
+    if (n_streams > 0 && (!table || !aligned4(table)))
+        return TF_EINVAL;
+    *p = PagesParams{};
+    p->refs = pages->refs;
+    p->n_pages = pages->n_pages;
+    p->P = pages->page_size;
+    p->table = table;
+    p->stride = stride;
+    p->S = n_streams;
+    p->status = status;
+    return TF_OK;
+}
+
+// Entries a list of `bytes` bytes can hold beside its head.
+int64_t move_cap(size_t bytes)
+{
+    const size_t n = bytes / TF_MOVE_BYTES;
+    return n == 0 ? -1 : n - 1 > INT32_MAX / 4 ? INT32_MAX / 4 : (int64_t)n - 1;
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? TF_OK : TF_ECUDA; }
+
 }  // namespace
 }  // namespace tfp
 
@@ -350,6 +382,69 @@ int tf_kv_put_rows(const tf_kv_pool *pool, const tf_streams *streams, const void
     p.S = streams->n_streams;
     p.W = rows;
     return launch_kv_put(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TF_OK : TF_ECUDA;
+}
+
+int tf_kv_put_rows_rope(const tf_kv_pool *pool, const tf_streams *streams, const tf_rope *rope,
+                        const int32_t *positions, const void *q, int64_t q_stride, void *q_out,
+                        int32_t n_q_heads, const void *k_rows, int64_t k_stride,
+                        const void *v_rows, int64_t v_stride, int32_t rows, void *stream)
+{
+    int rc = check_pool_streams(pool, streams);
+    if (rc != TF_OK)
+        return rc;
+    if (rows < 1 || streams->max_len < rows || n_q_heads < 0 || n_q_heads > (1 << 16) || !rope)
+        return TF_EINVAL;
+    if (rope->rotary_dim < 2 || rope->rotary_dim > pool->head_dim || rope->rotary_dim % 2 != 0 ||
+        rope->n_axes < 1 || rope->n_axes > 4 || (rope->adjacent != 0 && rope->adjacent != 1))
+        return TF_EINVAL;
+    RopeParams p;
+    for (int i = 0; i < 256; ++i)
+        p.pair_axis[i] = 0;
+    for (int i = 0; rope->pair_axis && i < rope->rotary_dim / 2; ++i) {
+        if (rope->pair_axis[i] >= rope->n_axes)
+            return TF_EINVAL;
+        p.pair_axis[i] = rope->pair_axis[i];
+    }
+    const int64_t q_row = (int64_t)n_q_heads * pool->head_dim;
+    const int64_t kv_row = (int64_t)pool->n_kv_heads * pool->head_dim;
+    if ((n_q_heads > 0 && (q_stride < q_row || q_stride % 8 != 0)) || k_stride < kv_row ||
+        k_stride % 8 != 0 || v_stride < kv_row || v_stride % 8 != 0)
+        return TF_EINVAL;
+    if (n_q_heads > 0 && q == q_out && q != nullptr && q_stride != q_row)
+        return TF_EINVAL;
+    if (streams->n_streams == 0)
+        return TF_OK;
+    if (!rope->inv_freq || !positions || !k_rows || !v_rows || !aligned16(k_rows) ||
+        !aligned16(v_rows))
+        return TF_EINVAL;
+    if (n_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out)))
+        return TF_EINVAL;
+    p.k_pool = static_cast<__nv_bfloat16 *>(pool->k_pool);
+    p.v_pool = static_cast<__nv_bfloat16 *>(pool->v_pool);
+    p.table = streams->table;
+    p.lens = streams->lens;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k_rows);
+    p.v = static_cast<const __nv_bfloat16 *>(v_rows);
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.positions = positions;
+    p.inv_freq = rope->inv_freq;
+    p.q_stride = n_q_heads > 0 ? q_stride : 0;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_pages = pool->n_pages;
+    p.Hkv = pool->n_kv_heads;
+    p.Hq = n_q_heads;
+    p.P = pool->page_size;
+    p.D = pool->head_dim;
+    p.table_stride = streams->table_stride;
+    p.S = streams->n_streams;
+    p.W = rows;
+    p.max_len = streams->max_len;
+    p.rotary = rope->rotary_dim;
+    p.n_axes = rope->n_axes;
+    p.adjacent = rope->adjacent;
+    return launch_kv_rope(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TF_OK : TF_ECUDA;
 }
 
 int tf_kv_copy_state(const tf_kv_pool *src_pool, const tf_streams *src,
@@ -398,6 +493,128 @@ int tf_kv_copy_state(const tf_kv_pool *src_pool, const tf_streams *src,
     p.chunk = copy_chunk_positions(p.D);
     p.n_chunks = (src->max_len + p.chunk - 1) / p.chunk;
     return launch_kv_copy(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TF_OK : TF_ECUDA;
+}
+
+int tf_kv_pages_fork(const tf_kv_pages *pages, const int32_t *src_table, int32_t src_stride,
+                     const int32_t *src_lens, int32_t n_src, const int32_t *parents, int32_t n_dst,
+                     int32_t *dst_table, int32_t dst_stride, int32_t *dst_lens, uint32_t *status,
+                     void *stream)
+{
+    PagesParams p;
+    const int rc =
+        check_pages(pages, const_cast<int32_t *>(src_table), src_stride, n_src, status, &p);
+    if (rc != TF_OK)
+        return rc;
+    if (n_dst < 0 || dst_stride < 1 || (int64_t)n_dst * dst_stride > INT32_MAX)
+        return TF_EINVAL;
+    if (n_src > 0 && !src_lens)
+        return TF_EINVAL;
+    if (n_dst == 0)
+        return TF_OK;
+    if (!parents || !dst_table || !dst_lens)
+        return TF_EINVAL;
+    p.lens = src_lens;
+    p.parents = parents;
+    p.dst_table = dst_table;
+    p.dst_lens = dst_lens;
+    p.dst_stride = dst_stride;
+    return status_of(launch_pages_fork(p, n_dst, static_cast<cudaStream_t>(stream)));
+}
+
+int tf_kv_pages_free(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                     int32_t n_streams, const int32_t *first, const int32_t *end, uint32_t *status,
+                     void *stream)
+{
+    PagesParams p;
+    const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
+    if (rc != TF_OK || n_streams == 0)
+        return rc;
+    p.first = first;
+    p.end = end;
+    return status_of(launch_pages_free(p, false, static_cast<cudaStream_t>(stream)));
+}
+
+int tf_kv_pages_free_window(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                            const int32_t *lens, int32_t n_streams, int32_t window, int32_t sinks,
+                            uint32_t *status, void *stream)
+{
+    PagesParams p;
+    const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
+    if (rc != TF_OK)
+        return rc;
+    if (window < 1 || sinks < 0 || (n_streams > 0 && !lens))
+        return TF_EINVAL;
+    if (n_streams == 0)
+        return TF_OK;
+    p.lens = lens;
+    p.window = window;
+    p.sinks = sinks;
+    return status_of(launch_pages_free(p, true, static_cast<cudaStream_t>(stream)));
+}
+
+int tf_kv_pages_grow(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                     const int32_t *lens, int32_t n_streams, int32_t rows, void *moves,
+                     size_t moves_bytes, uint32_t *status, void *stream)
+{
+    PagesParams p;
+    const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
+    if (rc != TF_OK)
+        return rc;
+    if (rows < 1 || (n_streams > 0 && !lens) || !moves || !aligned16(moves))
+        return TF_EINVAL;
+    const int64_t per_stream = ((int64_t)rows + p.P - 2) / p.P + 1;
+    const int64_t cap = move_cap(moves_bytes);
+    if (cap < 0 || per_stream * n_streams > cap)
+        return TF_ENOSPACE;
+    p.lens = lens;
+    p.rows = rows;
+    p.per_stream = static_cast<int32_t>(per_stream);
+    p.moves = static_cast<int4 *>(moves);
+    return status_of(launch_pages_grow(p, static_cast<cudaStream_t>(stream)));
+}
+
+int tf_kv_pages_compact(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,
+                        int32_t n_streams, void *moves, size_t moves_bytes, uint32_t *status,
+                        void *stream)
+{
+    PagesParams p;
+    const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
+    if (rc != TF_OK)
+        return rc;
+    if (!moves || !aligned16(moves))
+        return TF_EINVAL;
+    if (move_cap(moves_bytes) < p.n_pages / 2)
+        return TF_ENOSPACE;
+    p.moves = static_cast<int4 *>(moves);
+    return status_of(launch_pages_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+int tf_kv_pages_move(const tf_kv_pool *pool, const void *moves, size_t moves_bytes,
+                     uint32_t *status, void *stream)
+{
+    // (the pool's checks are those of a call without streams)
+    const tf_streams none{nullptr, 1, nullptr, 0, 1};
+    int rc = check_pool_streams(pool, &none);
+    if (rc != TF_OK)
+        return rc;
+    const int64_t cap = move_cap(moves_bytes);
+    if (!moves || !aligned16(moves) || cap < 0 || !aligned4(status))
+        return TF_EINVAL;
+    int sms = 0;
+    rc = device_sm_count(&sms);
+    if (rc != TF_OK)
+        return rc;
+    MoveParams p{};
+    p.k_pool = pool->k_pool;
+    p.v_pool = pool->v_pool;
+    p.moves = static_cast<const int32_t *>(moves);
+    p.status = status;
+    p.n_pages = pool->n_pages;
+    p.Hkv = pool->n_kv_heads;
+    p.P = pool->page_size;
+    p.D = pool->head_dim;
+    p.cap = static_cast<int32_t>(cap);
+    return status_of(launch_pages_move(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t tf_paged_attn_workspace_bytes(const tf_kv_pool *pool, const tf_streams *streams,

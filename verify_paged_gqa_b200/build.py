@@ -19,7 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "tfpaged")
 LIB = os.path.join(HERE, "libtfpaged.so")
-SOURCES = ["tf_paged.cu", "kv_put.cu", "kv_rope.cu", "kv_copy.cu", "kv_pages.cu", "attn_simt.cu",
+SOURCES = ["tf_paged.cu", "kv_put.cu", "kv_rope.cu", "kv_copy.cu", "kv_pages.cu", "attn_simt.cu", "attn_win.cu",
            "attn_prompt.cu", "attn_pm.cu", "attn_merge.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",

@@ -142,6 +142,13 @@ cudaError_t launch_pages_move(MoveParams p, int sms, cudaStream_t stream);
 // Rows per row block of the CUDA-core partial kernel.
 constexpr int kSimtRows = 4;
 
+// Sliding-window kernel of row blocks of 8 or 16 rows (attn_win.cu): grid =
+// units * p.whole blocks in clusters of p.whole = win_cluster_size, one per
+// unit.
+constexpr int kMaxCluster = 8;
+int win_cluster_size(const WinParams &p, int64_t units);
+cudaError_t launch_attn_win(const WinParams &p, int grid, cudaStream_t stream);
+
 template <int D>
 size_t simt_smem_bytes();
 template <int D>

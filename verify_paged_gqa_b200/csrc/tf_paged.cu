@@ -9,8 +9,10 @@
 #include "launch.cuh"
 #include "plan.cuh"
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 
 namespace tfp {
@@ -59,7 +61,7 @@ int check_pool_streams(const tf_kv_pool *pool, const tf_streams *st)
     return TF_OK;
 }
 
-enum class Kernel { kSimt, kPrompt, kPm };
+enum class Kernel { kSimt, kPrompt, kPm, kWin };
 
 // Workspace: the 256-byte header (status word, wait site, the launch's tile
 // count at byte 64), each stream's first tile (int64), then two partial slots
@@ -100,6 +102,17 @@ struct Plan {
     Kernel kernel;  // which partial kernel runs the call
 };
 
+bool pool_rows_past_31_bits(const tf_kv_pool *pool)
+{
+    return (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size > INT32_MAX;
+}
+
+bool takes_win_kernel(const WinParams &p)
+{
+    const char *e = getenv("WINK");
+    return e ? atoi(e) >= p.M : p.M <= 64;
+}
+
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
               int32_t rows_max, bool tree, Plan *plan, const Window *win = nullptr)
 {
@@ -118,14 +131,15 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         return TF_EINVAL;
     WinParams &p = plan->p;
     p = WinParams{};
+    p.P = pool->page_size;
     if (win) {
         // a window or sinks past every length see what max_len does
+        p.page_inv = p.P == 1 ? UINT32_MAX : (uint32_t)((1ull << 32) / p.P);
         p.window = win->window < st->max_len ? win->window : st->max_len;
         p.sinks = win->sinks < st->max_len ? win->sinks : st->max_len;
     }
     p.n_pages = pool->n_pages;
     p.Hkv = pool->n_kv_heads;
-    p.P = pool->page_size;
     p.D = pool->head_dim;
     p.table_stride = st->table_stride;
     p.S = st->n_streams;
@@ -169,10 +183,14 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     plan->kernel = Kernel::kSimt;
     p.RB = kSimtRows;
     if (win) {
-        // a sliding window: the tensor-core kernels (any row count and page
-        // size); pools past 2^31 rows are refused
+        // a sliding window; pools past 2^31 rows are refused
         const int nr = pm_rows(p);
-        if (nr > 0) {
+        if (pool_rows_past_31_bits(pool))
+            return TF_EUNSUPPORTED;
+        if (takes_win_kernel(p)) {
+            plan->kernel = Kernel::kWin;
+            p.RB = M <= 8 ? 8 : 16;
+        } else if (nr > 0) {
             plan->kernel = Kernel::kPm;
             p.RB = nr;
         } else if (prompt_supported(p)) {
@@ -236,6 +254,14 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     if (p.whole)
         grid = units > 0 ? units : 1;
     plan->grid = static_cast<int>(grid);
+    if (plan->kernel == Kernel::kWin) {
+        if (units > INT32_MAX / 8)
+            return TF_EINVAL;
+        p.whole = getenv("WINC") ? atoi(getenv("WINC")) : win_cluster_size(p, units);
+        plan->grid = static_cast<int>(units * p.whole);
+        plan->ws_bytes = kWsHeaderBytes;
+        return TF_OK;
+    }
     p.n_cta = plan->grid;
     plan->ws_bytes = ws_part_offset(p.S) + (size_t)2 * plan->grid * part_slot_floats(p) * sizeof(float);
     return TF_OK;
@@ -299,7 +325,9 @@ int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32
     p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (win) {
+    if (plan.kernel == Kernel::kWin) {
+        e = launch_attn_win(plan.p, plan.grid, s);
+    } else if (win) {
         e = launch_tensor_core(plan.p, plan, s);
     } else if (plan.kernel != Kernel::kSimt) {
         e = launch_tensor_core(p, plan, s);

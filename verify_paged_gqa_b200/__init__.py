@@ -24,5 +24,6 @@ __all__ = list(_EXPORTS)
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _abi
-        return getattr(_abi, name)
+        value = globals()[name] = getattr(_abi, name)   # found directly from now on
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -13,7 +13,9 @@ takes torch tensors in the layouts ``include/tf_paged.h`` documents:
 
 ``max_len`` is the host upper bound on lens (the launch is sized from it).
 Calls are asynchronous on ``stream`` (default: torch's current stream).  A
-non-zero status raises TFError.  ``raw`` is the loaded ctypes library, for
+non-zero status raises TFError.  The sliding-window, rotary and page calls are
+marshalled by the compiled module ``_binding`` (their host time counts), the
+others here with ctypes.  ``raw`` is the loaded ctypes library, for
 callers that hold plain device pointers.
 """
 from __future__ import annotations
@@ -82,6 +84,12 @@ class tf_kv_pages(ctypes.Structure):
 
 
 raw = ctypes.CDLL(library_path)
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"the compiled binding does not load ({e}): build it with "
+                      "`python -m verify_paged_gqa_b200.build` (there is no fallback path)") from e
+_binding.attach(library_path)
 _P = ctypes.POINTER
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 raw.tf_kv_put_rows.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _vp, _i32, _vp]
@@ -214,20 +222,7 @@ class Rope:
         self.struct = tf_rope(inv_freq.data_ptr(),
                               None if self._axes is None else ctypes.addressof(self._axes),
                               2 * pairs, self.n_axes, 1 if adjacent else 0)
-
-
-def _rows(t, heads, d, S, W, name):
-    """Pointer and row stride of step rows [S][W][heads][d] that may be slices
-    of a wider projection output: heads and dims dense, rows evenly apart."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 4:
-        raise TypeError(f"{name} must be a bfloat16 tensor with 4 dims")
-    if tuple(t.shape) != (S, W, heads, d):
-        raise ValueError(f"{name} must be [{S}][{W}][{heads}][{d}], not {list(t.shape)}")
-    st = t.stride()
-    row = st[1] if W > 1 else st[0] if S > 1 else heads * d
-    if ((d > 1 and st[3] != 1) or (heads > 1 and st[2] != d) or (W > 1 and S > 1 and st[0] != W * row)):
-        raise ValueError(f"{name}: heads and dims must be dense and rows evenly spaced")
-    return t.data_ptr(), row
+        self.address = ctypes.addressof(self.struct)
 
 
 def tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, positions, rope, max_len,
@@ -237,57 +232,13 @@ def tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, position
     their pages.  The rows may be slices of one projection's output.  Returns
     the turned queries (q_out, a new tensor by default, or q itself to turn
     them in place); q may be None."""
-    pool, st = _pool(k_pool, v_pool), _streams(table, lens, max_len)
-    _need(positions, torch.int32, 3, "positions")
-    if positions.shape[0] != st.n_streams or positions.shape[2] != rope.n_axes:
-        raise ValueError("positions must be [n_streams][rows][n_axes]")
-    S, W = st.n_streams, positions.shape[1]
-    hq, qp, qs, qo = 0, None, 0, None
-    if q is not None:
-        hq = q.shape[2] if q.dim() == 4 else 0
-        qp, qs = _rows(q, hq, pool.head_dim, S, W, "q")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _need(q_out, torch.bfloat16, 4, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        qo = q_out.data_ptr()
-    kp, ks = _rows(k_rows, pool.n_kv_heads, pool.head_dim, S, W, "k_rows")
-    vp, vs = _rows(v_rows, pool.n_kv_heads, pool.head_dim, S, W, "v_rows")
-    _check(raw.tf_kv_put_rows_rope(ctypes.byref(pool), ctypes.byref(st), ctypes.byref(rope.struct),
-                                   positions.data_ptr(), qp, qs, qo, hq, kp, ks, vp, vs, W,
-                                   _stream(stream)), "tf_kv_put_rows_rope")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    rc = _binding.tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, positions,
+                                      rope.address, max_len, q_out, stream)
+    if rc:
+        raise TFError(rc, "tf_kv_put_rows_rope")
     return q_out
-
-
-def _pages(refs, page_size):
-    _need(refs, torch.int32, 1, "refs")
-    return tf_kv_pages(refs.data_ptr(), refs.shape[0], int(page_size))
-
-
-def _row_ints(t, n, name):
-    """Pointer of an int32 tensor with one element per stream (None: null)."""
-    if t is None:
-        return None
-    _need(t, torch.int32, 1, name)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have one element per row")
-    return t.data_ptr()
-
-
-def _status(status):
-    if status is None:
-        return None
-    if status.dtype != torch.int32 or status.numel() < 1:
-        raise TypeError("status must be an int32 tensor")
-    return status.data_ptr()
-
-
-def _moves(moves):
-    _need(moves, torch.int32, 2, "moves")
-    if moves.shape[1] != 4:
-        raise ValueError("moves must be [1 + cap][4]")
-    return moves.data_ptr(), moves.shape[0] * TF_MOVE_BYTES
 
 
 def tf_kv_pages_fork(refs, page_size, src_table, src_lens, parents, dst_table, dst_lens,
@@ -296,68 +247,49 @@ def tf_kv_pages_fork(refs, page_size, src_table, src_lens, parents, dst_table, d
     (-1: none), each with one holder more in refs; dst_lens gets the lengths.
     status: optional int32 device tensor of one element that collects TF_DEV_*
     bits (every tf_kv_pages_* call takes one)."""
-    pg = _pages(refs, page_size)
-    _need(src_table, torch.int32, 2, "src_table")
-    _need(dst_table, torch.int32, 2, "dst_table")
-    n_src, n_dst = src_table.shape[0], dst_table.shape[0]
-    _check(raw.tf_kv_pages_fork(ctypes.byref(pg), src_table.data_ptr(), src_table.shape[1],
-                                _row_ints(src_lens, n_src, "src_lens"), n_src,
-                                _row_ints(parents, n_dst, "parents"), n_dst, dst_table.data_ptr(),
-                                dst_table.shape[1], _row_ints(dst_lens, n_dst, "dst_lens"),
-                                _status(status), _stream(stream)), "tf_kv_pages_fork")
+    rc = _binding.tf_kv_pages_fork(refs, page_size, src_table, src_lens, parents, dst_table,
+                                   dst_lens, status, stream)
+    if rc:
+        raise TFError(rc, "tf_kv_pages_fork")
 
 
 def tf_kv_pages_free(refs, page_size, table, first=None, end=None, status=None, stream=None):
     """Entries [first[s], end[s]) of the table's rows (default: all) give their
     pages back and hold -1."""
-    pg = _pages(refs, page_size)
-    _need(table, torch.int32, 2, "table")
-    n = table.shape[0]
-    _check(raw.tf_kv_pages_free(ctypes.byref(pg), table.data_ptr(), table.shape[1], n,
-                                _row_ints(first, n, "first"), _row_ints(end, n, "end"),
-                                _status(status), _stream(stream)), "tf_kv_pages_free")
+    rc = _binding.tf_kv_pages_free(refs, page_size, table, first, end, status, stream)
+    if rc:
+        raise TFError(rc, "tf_kv_pages_free")
 
 
 def tf_kv_pages_free_window(refs, page_size, table, lens, window, sinks, status=None, stream=None):
     """Frees the pages wholly behind every stream's sliding window (and past its sinks)."""
-    pg = _pages(refs, page_size)
-    _need(table, torch.int32, 2, "table")
-    n = table.shape[0]
-    _check(raw.tf_kv_pages_free_window(ctypes.byref(pg), table.data_ptr(), table.shape[1],
-                                       _row_ints(lens, n, "lens"), n, int(window), int(sinks),
-                                       _status(status), _stream(stream)),
-           "tf_kv_pages_free_window")
+    rc = _binding.tf_kv_pages_free_window(refs, page_size, table, lens, window, sinks, status,
+                                          stream)
+    if rc:
+        raise TFError(rc, "tf_kv_pages_free_window")
 
 
 def tf_kv_pages_grow(refs, page_size, table, lens, rows, moves, status=None, stream=None):
     """Gives the last ``rows`` positions of every stream pages of their own
     (copy on write); moves: int32 [1 + cap][4], the list for tf_kv_pages_move."""
-    pg = _pages(refs, page_size)
-    _need(table, torch.int32, 2, "table")
-    n = table.shape[0]
-    mp, mb = _moves(moves)
-    _check(raw.tf_kv_pages_grow(ctypes.byref(pg), table.data_ptr(), table.shape[1],
-                                _row_ints(lens, n, "lens"), n, int(rows), mp, mb, _status(status),
-                                _stream(stream)), "tf_kv_pages_grow")
+    rc = _binding.tf_kv_pages_grow(refs, page_size, table, lens, rows, moves, status, stream)
+    if rc:
+        raise TFError(rc, "tf_kv_pages_grow")
 
 
 def tf_kv_pages_compact(refs, page_size, table, moves, status=None, stream=None):
     """Moves the live pages to the lowest ids; refs and the table follow, moves
     gets the list for tf_kv_pages_move (its head: the moves, the live pages)."""
-    pg = _pages(refs, page_size)
-    _need(table, torch.int32, 2, "table")
-    mp, mb = _moves(moves)
-    _check(raw.tf_kv_pages_compact(ctypes.byref(pg), table.data_ptr(), table.shape[1],
-                                   table.shape[0], mp, mb, _status(status), _stream(stream)),
-           "tf_kv_pages_compact")
+    rc = _binding.tf_kv_pages_compact(refs, page_size, table, moves, status, stream)
+    if rc:
+        raise TFError(rc, "tf_kv_pages_compact")
 
 
 def tf_kv_pages_move(k_pool, v_pool, moves, status=None, stream=None):
     """Performs a list's page moves on one layer's pool."""
-    pool = _pool(k_pool, v_pool)
-    mp, mb = _moves(moves)
-    _check(raw.tf_kv_pages_move(ctypes.byref(pool), mp, mb, _status(status), _stream(stream)),
-           "tf_kv_pages_move")
+    rc = _binding.tf_kv_pages_move(k_pool, v_pool, moves, status, stream)
+    if rc:
+        raise TFError(rc, "tf_kv_pages_move")
 
 
 def tf_kv_copy_state(src_k, src_v, src_table, lens, dst_k, dst_v, dst_table, max_len,
@@ -390,7 +322,7 @@ def tf_paged_attn_workspace_bytes(k_pool, v_pool, table, lens, n_q_heads, rows, 
 
 
 def _attn(fn, name, k_pool, v_pool, table, lens, q, scale, out, workspace, max_len, stream,
-          with_rows, tree=None, window=()):
+          with_rows, tree=None):
     _need(q, torch.bfloat16, 4, "q")
     _need(out, torch.float32, 4, "out")
     if tuple(out.shape) != tuple(q.shape):
@@ -404,7 +336,6 @@ def _attn(fn, name, k_pool, v_pool, table, lens, q, scale, out, workspace, max_l
         args.append(q.shape[1])
     if tree is not None:
         args.append(tree.data_ptr())
-    args += window
     args += [float(scale), out.data_ptr(), workspace.data_ptr(), ws_bytes, _stream(stream)]
     _check(fn(*args), name)
     return out
@@ -460,20 +391,22 @@ def tf_paged_attn_decode_window(k_pool, v_pool, table, lens, q, window, sinks, s
                                 workspace, max_len, stream=None):
     """One query row per stream (q [S][1][Hq][d]) that sees the last ``window``
     positions and the first ``sinks`` ones."""
-    if q.shape[1] != 1:
-        raise ValueError("decode takes one row per stream")
-    return _attn(raw.tf_paged_attn_decode_window, "tf_paged_attn_decode_window", k_pool, v_pool,
-                 table, lens, q, scale, out, workspace, max_len, stream, with_rows=False,
-                 window=(int(window), int(sinks)))
+    rc = _binding.tf_paged_attn_decode_window(k_pool, v_pool, table, lens, q, window, sinks, scale,
+                                              out, workspace, max_len, stream)
+    if rc:
+        raise TFError(rc, "tf_paged_attn_decode_window")
+    return out
 
 
 def tf_paged_attn_verify_window(k_pool, v_pool, table, lens, q, window, sinks, scale, out,
                                 workspace, max_len, stream=None):
     """A causal draft window of q.shape[1] <= 8 rows per stream, each row
     seeing the last ``window`` positions and the first ``sinks`` ones."""
-    return _attn(raw.tf_paged_attn_verify_window, "tf_paged_attn_verify_window", k_pool, v_pool,
-                 table, lens, q, scale, out, workspace, max_len, stream, with_rows=True,
-                 window=(int(window), int(sinks)))
+    rc = _binding.tf_paged_attn_verify_window(k_pool, v_pool, table, lens, q, window, sinks, scale,
+                                              out, workspace, max_len, stream)
+    if rc:
+        raise TFError(rc, "tf_paged_attn_verify_window")
+    return out
 
 
 def tf_paged_attn_prompt_window(k_pool, v_pool, table, lens, q, window, sinks, scale, out,
@@ -481,9 +414,11 @@ def tf_paged_attn_prompt_window(k_pool, v_pool, table, lens, q, window, sinks, s
     """A chunk of q.shape[1] prompt rows per stream (the last rows of each
     stream), each row seeing the last ``window`` positions and the first
     ``sinks`` ones."""
-    return _attn(raw.tf_paged_attn_prompt_window, "tf_paged_attn_prompt_window", k_pool, v_pool,
-                 table, lens, q, scale, out, workspace, max_len, stream, with_rows=True,
-                 window=(int(window), int(sinks)))
+    rc = _binding.tf_paged_attn_prompt_window(k_pool, v_pool, table, lens, q, window, sinks, scale,
+                                              out, workspace, max_len, stream)
+    if rc:
+        raise TFError(rc, "tf_paged_attn_prompt_window")
+    return out
 
 
 def tf_testing_paged_attn(k_pool, v_pool, table, lens, q, scale, out, workspace, max_len,

@@ -1,4 +1,5 @@
-"""Builds libtfpaged.so (the C-ABI CUDA library) in place, for sm_100a only.
+"""Builds libtfpaged.so (the C-ABI CUDA library) in place, for sm_100a only, and
+_binding.so (torch tensors to that ABI) beside it.
 
     python -m verify_paged_gqa_b200.build [--verbose]
 
@@ -19,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "tfpaged")
 LIB = os.path.join(HERE, "libtfpaged.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["tf_paged.cu", "kv_put.cu", "kv_rope.cu", "kv_copy.cu", "kv_pages.cu", "attn_simt.cu", "attn_win.cu",
            "attn_prompt.cu", "attn_pm.cu", "attn_merge.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -40,9 +42,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -50,6 +52,27 @@ def up_to_date() -> bool:
 # an -Xcompiler value at commas)
 SANITIZE = ["-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
             "-fno-omit-frame-pointer"]
+
+
+def build_binding() -> None:
+    """Compile csrc/binding.cpp against the running interpreter's torch."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(verbose: bool = False, force: bool = False, sanitize: bool = False) -> str:
@@ -75,8 +98,11 @@ def build(verbose: bool = False, force: bool = False, sanitize: bool = False) ->
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = None if sanitize else ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
+        if binding is not None:
+            binding.result()
     log = "".join(out for _, out in results)
     with open(os.path.join(build_dir, "ptxas.log"), "w") as f:
         f.write(log)

@@ -12,7 +12,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdlib>
 #include <mutex>
 
 namespace tfp {
@@ -107,11 +106,8 @@ bool pool_rows_past_31_bits(const tf_kv_pool *pool)
     return (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size > INT32_MAX;
 }
 
-bool takes_win_kernel(const WinParams &p)
-{
-    const char *e = getenv("WINK");
-    return e ? atoi(e) >= p.M : p.M <= 64;
-}
+// Blocks of up to 16 rows take the cluster kernel (attn_win.cu).
+bool takes_win_kernel(const WinParams &p) { return p.M <= 16; }
 
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
               int32_t rows_max, bool tree, Plan *plan, const Window *win = nullptr)
@@ -257,7 +253,7 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     if (plan->kernel == Kernel::kWin) {
         if (units > INT32_MAX / 8)
             return TF_EINVAL;
-        p.whole = getenv("WINC") ? atoi(getenv("WINC")) : win_cluster_size(p, units);
+        p.whole = win_cluster_size(p, units);
         plan->grid = static_cast<int>(units * p.whole);
         plan->ws_bytes = kWsHeaderBytes;
         return TF_OK;

@@ -86,6 +86,26 @@ def test_rows_turned_and_written(d, rotary, adjacent, axes, W, P):
     RopeCase(3, W, 2, 3, d, P, rotary, axes, adjacent, seed=d + rotary + W).check()
 
 
+@pytest.mark.parametrize("d,rotary,adjacent", [(128, 128, False), (128, 64, True), (512, 208, False)])
+def test_rows_that_fill_the_gpu(d, rotary, adjacent):
+    """From 4,096 rows on a warp takes a row: the same bits as row by row."""
+    import verify_paged_gqa_b200 as tf
+    c = RopeCase(3, 1500, 2, 3, d, 64, rotary, 3, adjacent, seed=d)
+    q = tf.tf_kv_put_rows_rope(c.k_pool, c.v_pool, c.table, c.lens, c.q, c.k, c.v, c.positions, c.rope, c.max_len)
+    want, room = c.turned(c.q)
+    assert ((q.double() - want).abs() <= room).all()
+    pools = torch.zeros_like(c.k_pool), torch.zeros_like(c.v_pool)
+    for s in range(3):
+        one = tf.tf_kv_put_rows_rope(*pools, c.table[s:s + 1], c.lens[s:s + 1], c.q[s:s + 1], c.k[s:s + 1], c.v[s:s + 1],
+                                     c.positions[s:s + 1], c.rope, c.max_len)
+        assert torch.equal(one[0], q[s])
+        n = int(c.lens[s])
+        pos = torch.arange(n - 1500, n, device="cuda")
+        page, slot = c.table[s].long()[pos // 64], pos % 64
+        for a, b in zip((c.k_pool, c.v_pool), pools):
+            assert torch.equal(a[page, :, slot], b[page, :, slot])
+
+
 @pytest.mark.parametrize("far", [0, 1 << 20, 2 ** 31 - 1])
 def test_far_positions(far):
     RopeCase(4, 5, 1, 4, 128, 64, 128, 3, False, seed=far % 1000, far=far).check()

@@ -16,16 +16,19 @@
 // fp32, the products fp32, and each output is rounded once, to bf16.
 //
 // Memory bound: every input row is read once and every output written once.
-// One block per row: the row's rotary_dim / 2 angles are computed once, into
-// shared memory, and serve all its heads; a thread then moves 32 bytes (two
-// 16-byte vectors: 8 pairs) at a time.
+// The row's rotary_dim / 2 angles are computed once, into shared memory, and
+// serve all its heads; a thread moves 32 bytes (two 16-byte vectors: 8 pairs)
+// at a time, and the first loads are issued before the angles are formed.
 #include "launch.cuh"
+
+#include <algorithm>
 
 namespace tfp {
 
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int64_t kWarpRows = 4096;  // from so many rows on, one warp per row
 
 // The row's K/V destination (element offset of KV head 0), or -1: skipped.
 __device__ __forceinline__ int64_t row_slot(const RopeParams &p, int s, int r)
@@ -89,106 +92,160 @@ __device__ __forceinline__ void turn_adjacent(uint4 &a, const float2 *t)
     }
 }
 
-// kVec: rotary_dim is a multiple of 16, so that whole vectors are turned or
-// kept.  Otherwise each warp takes a head's row through shared memory, dim by
-// dim (every read comes before the row's writes, so q may be turned in place).
-template <bool kVec>
-__global__ void __launch_bounds__(kRopeThreads) kv_rope_kernel(const __grid_constant__ RopeParams p)
+// Where item `it` of a row lies: 32 bytes of a query head, a key head or a
+// value head, in this order.  `shift`: log2 of a head's items.
+struct Item {
+    int kind, h, c;  // 0: query, 1: key, 2: value; the head; its item
+    bool turned;
+    int d0, d1;      // first dims of its two vectors of 8
+};
+
+__device__ __forceinline__ Item item_of(const RopeParams &p, int it, int shift, int half)
 {
+    const int q_items = p.Hq << shift, k_items = p.Hkv << shift;
+    Item x;
+    x.kind = it < q_items ? 0 : it < q_items + k_items ? 1 : 2;
+    const int y = it - (x.kind == 0 ? 0 : x.kind == 1 ? q_items : q_items + k_items);
+    x.h = y >> shift;
+    x.c = y & ((1 << shift) - 1);
+    // dims (8c, half + 8c) of a turned half split, else 16 dims in a row
+    x.turned = x.kind != 2 && 8 * x.c < half;
+    x.d0 = x.turned && !p.adjacent ? 8 * x.c : 16 * x.c;
+    x.d1 = x.turned && !p.adjacent ? half + 8 * x.c : 16 * x.c + 8;
+    return x;
+}
+
+// rotary_dim a multiple of 16: whole vectors are turned or kept.  kGroup
+// threads take a row: a block's 256 while there are few rows, a warp once the
+// rows alone fill the GPU (no barriers then).  4,096 rows of 4 streams, 48
+// heads of 128 dims: 72 us by warps (5,560 GB/s), 84 by blocks.
+template <int kThreads, int kGroup>
+__global__ void __launch_bounds__(kThreads) kv_rope_kernel(const __grid_constant__ RopeParams p)
+{
+    constexpr int kGroups = kThreads / kGroup;
+    constexpr int kBatch = 2;  // items a thread has in flight
     allow_dependent_launch();  // the attention kernel after it may be scheduled now
-    __shared__ __align__(16) float2 turn[256];
-    __shared__ int64_t slot_sh;
-    __shared__ __align__(16) uint32_t stage[kVec ? 1 : kRopeThreads / 32][kVec ? 1 : 256];
+    __shared__ __align__(16) float2 turns[kGroups][256];
+    __shared__ int64_t slots[kGroups];
+    const int group = threadIdx.x / kGroup, lane = threadIdx.x % kGroup;
+    float2 *turn = turns[group];
     const int half = p.rotary / 2;
-    const int per = p.D / 16;  // 32-byte items per head
-    const int q_items = p.Hq * per, k_items = p.Hkv * per;
+    const int shift = 31 - __clz(p.D / 16);
+    const int n = (p.Hq + 2 * p.Hkv) << shift;
+    auto sync = [] {
+        if constexpr (kGroup == 32)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
     const int64_t rows = (int64_t)p.S * p.W;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const int s = static_cast<int>(row / p.W);
-        const int r = static_cast<int>(row - (int64_t)s * p.W);
-        __syncthreads();  // the previous row's angles are no longer read
-        if (threadIdx.x == kRopeThreads - 1)
-            slot_sh = row_slot(p, s, r);
-        for (int i = threadIdx.x; i < half; i += kRopeThreads)
-            turn[i] = pair_turn(p, p.positions + row * p.n_axes, i);
-        __syncthreads();
-        const int64_t slot = slot_sh;
+    for (int64_t row = (int64_t)blockIdx.x * kGroups + group; row < rows; row += (int64_t)gridDim.x * kGroups) {
         const __nv_bfloat16 *qs = p.q + row * p.q_stride, *ks = p.k + row * p.k_stride,
                             *vs = p.v + row * p.v_stride;
         __nv_bfloat16 *qd = p.q_out + row * p.Hq * p.D;
         const int64_t head_step = (int64_t)p.P * p.D;  // between a slot's KV heads
-        if constexpr (kVec) {
-            const int n = q_items + (slot >= 0 ? 2 * k_items : 0);
-            for (int it = threadIdx.x; it < n; it += kRopeThreads) {
-                const __nv_bfloat16 *src;
-                __nv_bfloat16 *dst;
-                int c;
-                bool turned = true;
-                if (it < q_items) {
-                    const int h = it / per;
-                    c = it - h * per;
-                    src = qs + h * p.D;
-                    dst = qd + h * p.D;
-                } else {
-                    int x = it - q_items;
-                    turned = x < k_items;
-                    x -= turned ? 0 : k_items;
-                    const int h = x / per;
-                    c = x - h * per;
-                    src = (turned ? ks : vs) + h * p.D;
-                    dst = (turned ? p.k_pool : p.v_pool) + slot + h * head_step;
+        int64_t slot = -1;
+        for (int base = 0; base < n; base += kBatch * kGroup) {
+            uint4 a[kBatch], b[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int it = base + k * kGroup + lane;
+                if (it < n) {
+                    const Item x = item_of(p, it, shift, half);
+                    const __nv_bfloat16 *src = (x.kind == 0 ? qs : x.kind == 1 ? ks : vs) + x.h * p.D;
+                    // (not __ldg: q may be its own output)
+                    a[k] = *reinterpret_cast<const uint4 *>(src + x.d0);
+                    b[k] = *reinterpret_cast<const uint4 *>(src + x.d1);
                 }
-                // the item's two vectors: dims (8c, half + 8c) of a turned half
-                // split, else 16 dims in a row
-                const bool inside = turned && 8 * c < half;
-                int d0 = 16 * c, d1 = 16 * c + 8;
-                if (inside && !p.adjacent) {
-                    d0 = 8 * c;
-                    d1 = half + 8 * c;
+            }
+            if (base == 0) {
+                // the row's angles and slot, while its first items are on their way
+                sync();  // (the previous row's are no longer read)
+                if (lane == kGroup - 1) {
+                    const int s = static_cast<int>(row / p.W);
+                    slots[group] = row_slot(p, s, static_cast<int>(row - (int64_t)s * p.W));
                 }
-                uint4 a = *reinterpret_cast<const uint4 *>(src + d0);  // (not __ldg: q may be its own output)
-                uint4 b = *reinterpret_cast<const uint4 *>(src + d1);
-                if (inside) {
+                for (int i = lane; i < half; i += kGroup)
+                    turn[i] = pair_turn(p, p.positions + row * p.n_axes, i);
+                sync();
+                slot = slots[group];
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int it = base + k * kGroup + lane;
+                if (it >= n)
+                    continue;
+                const Item x = item_of(p, it, shift, half);
+                if (x.kind != 0 && slot < 0)
+                    continue;
+                if (x.turned) {
                     if (p.adjacent) {
-                        turn_adjacent(a, turn + 8 * c);
-                        turn_adjacent(b, turn + 8 * c + 4);
+                        turn_adjacent(a[k], turn + 8 * x.c);
+                        turn_adjacent(b[k], turn + 8 * x.c + 4);
                     } else {
-                        turn_halves(a, b, turn + 8 * c);
+                        turn_halves(a[k], b[k], turn + 8 * x.c);
                     }
                 }
-                *reinterpret_cast<uint4 *>(dst + d0) = a;
-                *reinterpret_cast<uint4 *>(dst + d1) = b;
+                __nv_bfloat16 *dst = x.kind == 0 ? qd + x.h * p.D
+                                                 : (x.kind == 1 ? p.k_pool : p.v_pool) + slot + x.h * head_step;
+                *reinterpret_cast<uint4 *>(dst + x.d0) = a[k];
+                *reinterpret_cast<uint4 *>(dst + x.d1) = b[k];
             }
-        } else {
-            const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-            const int heads = p.Hq + (slot >= 0 ? 2 * p.Hkv : 0);
-            for (int h = warp; h < heads; h += kRopeThreads / 32) {
-                const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-                const int hk = h - p.Hq - (is_k ? 0 : p.Hkv);
-                const __nv_bfloat16 *src = is_q ? qs + (int64_t)h * p.D : (is_k ? ks : vs) + (int64_t)hk * p.D;
-                __nv_bfloat16 *dst = is_q ? qd + (int64_t)h * p.D
-                                          : (is_k ? p.k_pool : p.v_pool) + slot + hk * head_step;
-                for (int w = lane; w < p.D / 2; w += 32)
-                    stage[warp][w] = reinterpret_cast<const uint32_t *>(src)[w];
-                __syncwarp();
-                auto at = [&](int d) { return d & 1 ? bf_hi(stage[warp][d >> 1]) : bf_lo(stage[warp][d >> 1]); };
-                // the turned value of dim d < rotary
-                auto value = [&](int d) {
-                    const bool second = p.adjacent ? (d & 1) != 0 : d >= half;
-                    const int i = p.adjacent ? d >> 1 : second ? d - half : d;
-                    const float2 t = turn[i];
-                    const int other = p.adjacent ? d ^ 1 : second ? d - half : d + half;
-                    return second ? turn_b(at(other), at(d), t) : turn_a(at(d), at(other), t);
-                };
-                for (int w = lane; w < p.D / 2; w += 32) {
-                    const int d = 2 * w;  // rotary is even: both dims are turned, or neither
-                    uint32_t word = stage[warp][w];
-                    if ((is_q || is_k) && d < p.rotary)
-                        word = pack2(value(d), value(d + 1));
-                    reinterpret_cast<uint32_t *>(dst)[w] = word;
-                }
-                __syncwarp();
+        }
+    }
+}
+
+// Any other rotary_dim: one block per row, whose warps take a head each
+// through shared memory, dim by dim (every read comes before the row's
+// writes, so q may be turned in place).
+__global__ void __launch_bounds__(kRopeThreads) kv_rope_odd_kernel(const __grid_constant__ RopeParams p)
+{
+    allow_dependent_launch();
+    __shared__ __align__(16) float2 turn[256];
+    __shared__ int64_t slot_sh;
+    __shared__ __align__(16) uint32_t stage[kRopeThreads / 32][256];
+    const int half = p.rotary / 2;
+    const int64_t rows = (int64_t)p.S * p.W;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        __syncthreads();  // the previous row's angles are no longer read
+        if (threadIdx.x == kRopeThreads - 1) {
+            const int s = static_cast<int>(row / p.W);
+            slot_sh = row_slot(p, s, static_cast<int>(row - (int64_t)s * p.W));
+        }
+        for (int i = threadIdx.x; i < half; i += kRopeThreads)
+            turn[i] = pair_turn(p, p.positions + row * p.n_axes, i);
+        __syncthreads();
+        const int64_t slot = slot_sh;
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const int heads = p.Hq + (slot >= 0 ? 2 * p.Hkv : 0);
+        for (int h = warp; h < heads; h += kRopeThreads / 32) {
+            const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+            const int hk = h - p.Hq - (is_k ? 0 : p.Hkv);
+            const __nv_bfloat16 *src = is_q   ? p.q + row * p.q_stride + (int64_t)h * p.D
+                                       : is_k ? p.k + row * p.k_stride + (int64_t)hk * p.D
+                                              : p.v + row * p.v_stride + (int64_t)hk * p.D;
+            __nv_bfloat16 *dst = is_q ? p.q_out + (row * p.Hq + h) * p.D
+                                      : (is_k ? p.k_pool : p.v_pool) + slot + (int64_t)hk * p.P * p.D;
+            for (int w = lane; w < p.D / 2; w += 32)
+                stage[warp][w] = reinterpret_cast<const uint32_t *>(src)[w];
+            __syncwarp();
+            auto at = [&](int d) { return d & 1 ? bf_hi(stage[warp][d >> 1]) : bf_lo(stage[warp][d >> 1]); };
+            // the turned value of dim d < rotary
+            auto value = [&](int d) {
+                const bool second = p.adjacent ? (d & 1) != 0 : d >= half;
+                const int i = p.adjacent ? d >> 1 : second ? d - half : d;
+                const float2 t = turn[i];
+                const int other = p.adjacent ? d ^ 1 : second ? d - half : d + half;
+                return second ? turn_b(at(other), at(d), t) : turn_a(at(d), at(other), t);
+            };
+            for (int w = lane; w < p.D / 2; w += 32) {
+                const int d = 2 * w;  // rotary is even: both dims are turned, or neither
+                uint32_t word = stage[warp][w];
+                if ((is_q || is_k) && d < p.rotary)
+                    word = pack2(value(d), value(d + 1));
+                reinterpret_cast<uint32_t *>(dst)[w] = word;
             }
+            __syncwarp();
         }
     }
 }
@@ -200,11 +257,16 @@ cudaError_t launch_kv_rope(const RopeParams &p, cudaStream_t stream)
     const int64_t rows = (int64_t)p.S * p.W;
     if (rows == 0)
         return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>(rows < 0x7fffffff ? rows : 0x7fffffff);
-    if (p.rotary % 16 == 0)
-        kv_rope_kernel<true><<<grid, kRopeThreads, 0, stream>>>(p);
-    else
-        kv_rope_kernel<false><<<grid, kRopeThreads, 0, stream>>>(p);
+    const int64_t most = 0x7fffffff;
+    if (p.rotary % 16 != 0) {
+        kv_rope_odd_kernel<<<static_cast<unsigned>(std::min(rows, most)), kRopeThreads, 0, stream>>>(p);
+    } else if (rows < kWarpRows) {
+        kv_rope_kernel<kRopeThreads, kRopeThreads><<<static_cast<unsigned>(rows), kRopeThreads, 0, stream>>>(p);
+    } else {
+        constexpr int threads = 128, per_block = threads / 32;
+        kv_rope_kernel<threads, 32><<<static_cast<unsigned>(std::min((rows + per_block - 1) / per_block, most)),
+                                      threads, 0, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 

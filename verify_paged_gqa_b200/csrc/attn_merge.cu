@@ -65,12 +65,20 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         }
         return;
     }
-    if (p.whole)
+    if (p.whole == 1)
         return;  // every unit was finished whole by one CTA
     // the unit's tiles [U0, U1) and the CTAs that met them: warp 0 works them
     // out once for the block (lanes split the row blocks)
     __shared__ int nseg_sh;
-    if (warp == 0) {
+    if (p.whole) {
+        // piece k of the unit left its partial in its CTA's first slot
+        const int n = unit_tiles(p, len, b);
+        const int c0 = (u * p.n_rblk + b) * p.whole;
+        for (int k = threadIdx.x; k < p.whole; k += blockDim.x)
+            slots[k] = piece_start(n, k, p.whole) < piece_start(n, k + 1, p.whole) ? 2 * (c0 + k) : -1;
+        if (threadIdx.x == 0)
+            nseg_sh = n > 1 ? p.whole : 0;  // (one tile: one piece finished the unit)
+    } else if (warp == 0) {
         long long hw = 0, before = 0;
         for (int bb = lane; bb < p.n_rblk; bb += 32) {
             const int t = unit_work(p, len, bb);

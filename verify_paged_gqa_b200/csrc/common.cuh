@@ -55,7 +55,7 @@ struct AttnParams {
     int32_t SR;                 // rows per partial slot: min(RB, M)
     int32_t n_cta;              // persistent CTAs of the partial kernel (the work split)
     int32_t VT;                 // entry tiles of work in front of every unit
-    int32_t whole;              // 1: CTA c takes unit c whole (no split, no partials)
+    int32_t whole;              // > 0: every unit is cut into `whole` pieces, one to a CTA
     int32_t has_tree;           // 1: tree-verify call (the tree pointer holds the masks)
     // Test switch (0 in every library call): 1 makes CTA 0 withhold one
     // synchronous arrival that no copy or MMA completes -- the softmax warps'

@@ -22,7 +22,10 @@
 // two units partially).  The merge kernel finds a split unit's segments from
 // the same arithmetic and combines them in position order.  (When the call's
 // units fill most CTAs but not more, the tensor-bound prompt kernel instead
-// gives CTA c unit c whole: no partials and no merge.)  A unit's result
+// gives CTA c unit c whole: no partials and no merge.  A sliding-window call
+// with fewer units than CTAs cuts each unit into the same number of pieces,
+// one to a CTA: its units are short, and a CTA whose range crossed into a
+// second one would pay two starts on the call's critical path.)  A unit's result
 // therefore depends on the lengths of the call's streams and the grid size
 // (never on the page table, nor on run-to-run timing).
 //
@@ -119,6 +122,12 @@ __host__ __device__ __forceinline__ int cta_of(int64_t g, int64_t tot, int n_cta
     return static_cast<int>((g * n_cta + n_cta - 1) / tot);
 }
 
+// First tile of piece j of a unit's n tiles, cut into `pieces`.
+__host__ __device__ __forceinline__ int piece_start(int n, int j, int pieces)
+{
+    return static_cast<int>((int64_t)n * j / pieces);
+}
+
 // This CTA's range, found by warp 0 at kernel start.
 struct CtaRange {
     long long g0, g1;   // work tiles [g0, g1) of the launch
@@ -135,9 +144,10 @@ template <class P>
 __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
 {
     if (p.whole) {
-        // CTA c takes unit c (stream, KV head, row block) whole
+        // CTA c takes piece c mod whole of unit c / whole (stream, KV head, row
+        // block): the unit's tiles in `whole` runs of nearly equal length
         const int per_s = p.Hkv * p.n_rblk;
-        const int c = blockIdx.x;
+        const int c = blockIdx.x / p.whole;
         const int s = c / per_s;
         const int len = s < p.S ? __ldg(p.lens + s) : 0;
         const long long hw = s < p.S ? head_work(p, len) : 0;
@@ -152,9 +162,14 @@ __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
                 long long before = 0;
                 for (int bb = 0; bb < b; ++bb)
                     before += unit_work(p, len, bb);
-                out.s0 = s;
-                out.off0 = kh * hw + before;
-                out.g1 = unit_work(p, len, b);
+                const int j = blockIdx.x % p.whole;
+                const int n = unit_tiles(p, len, b);
+                const int t0 = piece_start(n, j, p.whole), t1 = piece_start(n, j + 1, p.whole);
+                if (t1 > t0) {
+                    out.s0 = s;
+                    out.off0 = kh * hw + before + p.VT + t0;
+                    out.g1 = t1 - t0;
+                }
             }
         }
         return;

@@ -247,8 +247,17 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     const int64_t units = (int64_t)p.S * p.Hkv * p.n_rblk;
     const int cap = sms < kMaxCtas ? sms : kMaxCtas;
     p.whole = plan->kernel == Kernel::kPrompt && units <= cap && 4 * units >= 3 * (int64_t)cap;
+    // A sliding-window call on the position-major kernel with fewer units than
+    // CTAs: as many whole pieces per unit as there are CTAs for, if that uses
+    // three quarters of them.
+    if (win && plan->kernel == Kernel::kPm && units > 0 && units <= cap) {
+        const int64_t tiles = head_work(p, st->max_len) / p.n_rblk - p.VT + 1;
+        const int64_t pieces = std::min<int64_t>(cap / units, tiles);
+        if (4 * units * pieces >= 3 * (int64_t)cap || pieces == tiles)
+            p.whole = static_cast<int32_t>(pieces);
+    }
     if (p.whole)
-        grid = units > 0 ? units : 1;
+        grid = units > 0 ? units * p.whole : 1;
     plan->grid = static_cast<int>(grid);
     if (plan->kernel == Kernel::kWin) {
         if (units > INT32_MAX / 8)

@@ -2,44 +2,44 @@
 // query rows per KV head: decode, draft-verify windows, short prompt chunks.
 //
 // A window bounds what a block reads (window + sinks positions), so such a
-// call is short, and what counts is that every SM has loads in flight soon and
-// that nothing follows them.  One launch:
+// call is short and what counts is its latency and that every SM has loads in
+// flight from the first microsecond on.  The kernel therefore has no producer,
+// no ring and no second launch:
 //
 //   split    a unit (stream, KV head, row block) is one cluster of C thread
-//            blocks, one block to an SM, each with a run of the unit's tiles.
-//            C comes from the host's arguments (win_cluster_size).
-//   loads    a producer warp fills a ring of 192 KB with TMA boxes: units of a
-//            tile's positions x 128 dims (two boxes of 64 dims, 128-byte
-//            swizzle), K of every slice of 128 dims, then V.  A tile is 128
-//            positions (64 at head dim 512, so that 1.5 tiles fit).  Tiles are
-//            assembled from page pieces (ring.cuh), and rows between the
-//            sinks and the window, or past the stream's end, are not loaded.
-//            (Fragments copied by the lanes with cp.async instead spent 55% of
-//            a warp's time on issuing the copies: 12 streams x 4,100 positions
-//            47 us.)
-//   products eight consumer warps, each with 16 positions of a tile at a time:
-//            mma.sync m16n8k16 with positions, then dims, on the 16 rows of A
-//            and query rows on the 8 columns of B: S^T = K Q^T, O^T = V^T P^T, so
-//            a decode block of up to 8 rows fills the instruction, and a warp
-//            needs nothing from another until the end.  The order of a
-//            contraction's terms is free, so dims are permuted to make each
-//            lane's fragment 16 contiguous bytes of a K row, and output dims to
-//            make it 16 contiguous bytes of a V row; positions are permuted so
-//            that eight lanes' rows fall on all banks of the swizzled tile.  P
-//            goes from one layout to the other with 8 x 8 transposes in
-//            registers, in three bf16 parts (24 bits), and each product is
-//            added to O in fp32 with rounding (the tensor cores truncate their
-//            sums: chained over 2,048 positions that was 6e-6 of the output's
-//            norm; now 3e-7).
-//   join     each warp leaves its O, the groups of warps their maxima and sums
-//            in shared memory; after one cluster barrier the cluster's blocks
-//            combine them over distributed shared memory, each a share of the
-//            output.
+//            blocks; its positions are dealt out in chunks of 16 to the
+//            cluster's 4 C / (D / 128) teams of warps, chunk k to team k mod
+//            (teams).  C comes from the host's arguments (launch rule below).
+//   loads    asynchronous 16-byte copies into each warp's own ring in shared
+//            memory, two or three chunks deep (192 KB in flight per SM): K by
+//            fragments (a lane copies what it reads back, 512 contiguous bytes a
+//            warp), V by rows.  Only rows that some query row sees are read;
+//            pages cost one table lookup per position, a chunk ahead.
+//   products S^T = K Q^T: mma.sync m16n8k16 with positions on the 16 rows of A and
+//            query rows on the 8 columns of B, so a decode block of up to 8 rows
+//            fills the instruction; the order of a contraction's terms is free,
+//            so dims are permuted to make each lane's fragment 16 contiguous
+//            bytes of a K row.
+//            O += P V, up to 8 rows: packed fp32 FMAs over two rows, P in fp32
+//            through shared memory; half a warp takes the even positions, the
+//            other half the odd ones, eight dims a lane.  (mma.sync runs at a
+//            quarter of its nominal rate here, 32 cycles per scheduler: with P
+//            in three bf16 parts, for the same accuracy, PV took 192 cycles
+//            per SM and chunk, these FMAs take 64.)
+//            16 rows, whose sums would not fit the registers that way: O^T = V^T
+//            P^T with mma.sync, P in three bf16 parts (24 bits) moved from one
+//            fragment layout to the other by 8 x 8 transposes, V in fragments as
+//            K; each chunk's product is added to O in fp32 with rounding (the
+//            tensor cores truncate their sums: chained over 128 chunks that
+//            was 6e-6 of the output's norm, now 3e-7).
+//   join     each warp leaves its O, the teams their maxima and sums in shared
+//            memory; after one cluster barrier the cluster's blocks combine
+//            them over distributed shared memory, each a share of the output.
 //
-// D = 256 and 512: the warps are split over D / 128 slices of the dims as well;
-// the warps that share positions sum their scores through shared memory.
+// D = 256 and 512: a team is D / 128 warps that share positions and split the
+// dims; the chunk's scores are summed over the team through shared memory.
 #include "launch.cuh"
-#include "ring.cuh"
+#include "plan.cuh"
 
 #include <algorithm>
 
@@ -47,11 +47,15 @@ namespace tfp {
 
 namespace {
 
-constexpr int kConsumers = 8;                       // warps; one more produces
-constexpr int kWinThreads = 32 * (kConsumers + 1);
-constexpr int kChunk = 16;                          // positions a warp takes at a time
-constexpr uint32_t kRingBytes = 196608;
-constexpr float kRescaleLog2 = 8.f;                 // move a row's reference max only past this growth
+constexpr int kWinThreads = 128;
+constexpr int kWinWarps = kWinThreads / 32;
+constexpr int kChunk = 16;               // positions a team takes at a time
+// Blocks per SM and chunks in flight per warp: either way 192 KB in flight.
+// (A warp's own chain of latencies bounds a chunk, so up to eight rows, whose
+// registers allow it, run twelve warps on an SM.)
+constexpr int win_blocks(int R) { return R <= 8 ? 3 : 2; }
+constexpr int win_stages(int R) { return R <= 8 ? 2 : 3; }
+constexpr float kRescaleLog2 = 8.f;      // move a row's reference max only past this growth
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1)
@@ -62,12 +66,40 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Copies 16 bytes to shared memory asynchronously, or zeroes them (nothing is
+// read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16 *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+
 // An 8 x 8 matrix of 16-bit values, two neighbours of a row per lane, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t a)
 {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
+}
+
+// Two probabilities as three bf16 pairs, each rounded to nearest: p = hi + mid
+// + lo to 2^-26 p.
+__device__ __forceinline__ void split3(float p0, float p1, uint32_t (&part)[3])
+{
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(part[0]) : "f"(p1), "f"(p0));
+    const float r0 = p0 - bf_lo(part[0]), r1 = p1 - bf_hi(part[0]);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(part[1]) : "f"(r1), "f"(r0));
+    const float q0 = r0 - bf_lo(part[1]), q1 = r1 - bf_hi(part[1]);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(part[2]) : "f"(q1), "f"(q0));
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until at most N of the thread's groups of copies are in flight.
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -100,207 +132,44 @@ __device__ __forceinline__ float4 peer_f32x4(uint32_t addr)
     return v;
 }
 
-// Two probabilities as three bf16 pairs, each rounded to nearest: p = hi + mid
-// + lo to 2^-26 p.
-__device__ __forceinline__ void split3(float p0, float p1, uint32_t &hi, uint32_t &mid, uint32_t &lo)
-{
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
-    const float r0 = p0 - bf_lo(hi), r1 = p1 - bf_hi(hi);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(mid) : "f"(r1), "f"(r0));
-    const float q0 = r0 - bf_lo(mid), q1 = r1 - bf_hi(mid);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(q1), "f"(q0));
-}
-
-template <int D>
-struct WinShape {
-    static constexpr int T = D == 512 ? 64 : 128;             // positions of a tile
-    static constexpr int kSlices = D / 128;
-    static constexpr int kGroups = kConsumers / kSlices;      // groups of warps with the same positions
-    static constexpr int CW = T / kChunk / kGroups;           // chunks of a tile per warp
-    static constexpr uint32_t kBox = T * 128, kUnit = 2 * kBox;
-    static constexpr int NU = kRingBytes / kUnit;             // ring units
-    static constexpr int kHeights = D == 512 ? 7 : 8;         // boxes of 1, 2, 4, ..., T rows
-    static_assert(NU >= 2 * kSlices, "a tile's K and V units fit the ring");
-};
-
-template <int D, int NT>
+template <int D, int R>
 struct WinSmem {
-    using W = WinShape<D>;
-    // at the end, the consumer warps' unnormalised outputs [8 NT rows][128]
-    alignas(1024) uint8_t ring[W::NU][W::kUnit];
-    // the slices' partial scores, by parity of the tile
-    alignas(16) float s[W::kSlices > 1 ? 2 : 1][W::kSlices > 1 ? kConsumers : 1][W::CW][32][4 * NT];
-    float m[W::kGroups][8 * NT];   // reference maxima, log2 units
-    float l[W::kGroups][8 * NT];   // sums
-    uint64_t full[W::NU];
-    uint64_t empty[W::NU];
-    volatile int abort_flag;
-    long long wait_limit;
+    static constexpr int kTeam = D / 128;               // warps per team
+    static constexpr int kTeams = kWinWarps / kTeam;
+    // a warp's ring: [stage][K fragments [copy][lane], V rows [position][128]]; at
+    // its end, the warp's unnormalised output [row][128]
+    alignas(16) uint4 ring[kWinWarps][win_stages(R)][2][8][32];
+    // the team's partial scores, by parity of the chunk
+    alignas(16) float s[kTeam > 1 ? 2 : 1][kTeam > 1 ? kWinWarps : 1][kTeam > 1 ? 32 : 1][R == 16 ? 8 : 4];
+    alignas(16) float p[kWinWarps][kChunk][R <= 8 ? R : 4];  // a warp's probabilities (FMAs)
+    alignas(16) float alpha[kWinWarps][R <= 8 ? R : 4];      // factors of the last change of reference
+    float m[kTeams][R];                                 // reference maxima, log2 units
+    float l[kTeams][R];                                 // sums
 };
 
-template <int D, int NT>
-constexpr size_t win_smem_bytes()
+// R: rows of a block (p.RB): 4, 8 or 16.
+template <int D, int R>
+__global__ void __launch_bounds__(kWinThreads, win_blocks(R)) attn_win_kernel(const __grid_constant__ WinParams p)
 {
-    return sizeof(WinSmem<D, NT>) + 1024;  // + alignment slack
-}
-
-template <int D>
-struct WinArgs {
-    WinParams p;
-    CUtensorMap kmap[WinShape<D>::kHeights];
-    CUtensorMap vmap[WinShape<D>::kHeights];
-};
-
-// The unit's piece of this block: tiles [t0, t1) of squeezed positions.
-struct Piece {
-    WorkItem it;
-    int t0, t1;
-};
-
-// One page's rows of a tile: rows [row, row + n) come from pool rows y on.
-struct Rows {
-    int row, n, y;
-};
-
-// Piece i of a tile (its pages in order, those of the run before the skipped
-// positions first); n = 0 past the last one.
-__device__ __forceinline__ Rows tile_piece(const WinParams &p, const Piece &pc, const int32_t *trow, int tpos,
-                                           int nvalid, int i, int *pieces)
-{
-    const TileRows rows = tile_rows(p, pc.it, tpos, nvalid);
-    const int pos_b = tpos + rows.b + pc.it.skip;
-    const int lp_a = tpos / p.P, lp_b = pos_b / p.P;
-    const int off_a = tpos - lp_a * p.P, off_b = pos_b - lp_b * p.P;
-    const int n_a = rows.a > 0 ? (off_a + rows.a - 1) / p.P + 1 : 0;
-    const int n_b = nvalid > rows.b ? (off_b + nvalid - rows.b - 1) / p.P + 1 : 0;
-    *pieces = n_a + n_b;
-    Rows x = {0, 0, 0};
-    if (i < n_a + n_b) {
-        const bool first = i < n_a;
-        const int k = first ? i : i - n_a;
-        const int off = first ? off_a : off_b;
-        const int slot = k == 0 ? off : 0;
-        x.row = (first ? 0 : rows.b) + (k == 0 ? 0 : k * p.P - off);
-        x.n = min((first ? rows.a : nvalid) - x.row, p.P - slot);
-        int page = __ldg(trow + (first ? lp_a : lp_b) + k);
-        if (page < 0 || page >= p.n_pages) {
-            // never read: page 0 stands in (the stream's outputs are flagged)
-            set_flag(p.flags, kDevBadPage);
-            page = 0;
-        }
-        x.y = (page * p.Hkv + pc.it.kh) * p.P + slot;
-    }
-    return x;
-}
-
-// The whole producer warp: lane i copies piece i of every tile (a tile in
-// pages of fewer than 4 positions has more than 32: the lanes go round).
-template <int D, int NT>
-__device__ __forceinline__ void win_producer(const WinArgs<D> &a, WinSmem<D, NT> &sm, const Piece &pc, int lane)
-{
-    using W = WinShape<D>;
-    const WinParams &p = a.p;
-    // row blocks of a unit read the same pages: keep them in L2 for each other
-    uint64_t pol;
-    if (p.n_rblk > 1)
-        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    else
-        pol = l2_evict_first_policy();
-    const int32_t *trow = p.table + (int64_t)pc.it.s * p.table_stride;
-    auto nvalid = [&](int t) { return min(W::T, pc.it.len - t * W::T); };
-    uint32_t U = 0;  // units issued
-    bool ok = true;
-    int pieces, pieces_next = 0;
-    Rows now = tile_piece(p, pc, trow, pc.t0 * W::T, nvalid(pc.t0), lane, &pieces);
-    for (int t = pc.t0; ok && t < pc.t1; ++t) {
-        // (the next tile's page ids are read while this one's units wait for room)
-        Rows next = now;
-        if (t + 1 < pc.t1)
-            next = tile_piece(p, pc, trow, (t + 1) * W::T, nvalid(t + 1), lane, &pieces_next);
-        const TileRows rows = tile_rows(p, pc.it, t * W::T, nvalid(t));
-        const uint32_t bytes = (uint32_t)(rows.a + nvalid(t) - rows.b) * 256u;
-#pragma unroll 1
-        for (int x = 0; x < 2 * W::kSlices; ++x) {
-            const int st = (int)(U % W::NU);
-            if (lane == 0) {
-                ok = pwait(sm, &sm.empty[st], ((U / W::NU) & 1u) ^ 1u, p.flags, kWaitEmpty);
-                if (ok)
-                    mbar_arrive_expect_tx(&sm.full[st], bytes);
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok)
-                break;
-            const CUtensorMap *maps = x < W::kSlices ? a.kmap : a.vmap;
-            const int dim = 128 * (x % W::kSlices);
-            Rows cur = now;
-            for (int i = lane;;) {
-                // one box for each set bit of n
-                while (cur.n > 0) {
-                    const int h = 31 - __clz(cur.n);
-                    uint8_t *dst = sm.ring[st] + cur.row * 128;
-                    tma_load_2d(dst, &maps[h], dim, cur.y, &sm.full[st], pol);
-                    tma_load_2d(dst + W::kBox, &maps[h], dim + 64, cur.y, &sm.full[st], pol);
-                    cur.row += 1 << h;
-                    cur.y += 1 << h;
-                    cur.n -= 1 << h;
-                }
-                i += 32;
-                if (i >= pieces)
-                    break;
-                int again;
-                cur = tile_piece(p, pc, trow, t * W::T, nvalid(t), i, &again);
-            }
-            __syncwarp();
-            ++U;
-        }
-        now = next;
-        pieces = pieces_next;
-    }
-    if (lane == 0) {
-        // let the copies in flight land before the block can exit
-        for (uint32_t k = 1; k <= (U < (uint32_t)W::NU ? U : (uint32_t)W::NU); ++k)
-            (void)mbar_wait(&sm.full[(U - k) % W::NU], ((U - k) / W::NU) & 1u, sm.wait_limit);
-    }
-    __syncwarp();
-}
-
-// NT: tiles of 8 query rows.
-template <int D, int NT>
-__global__ void __launch_bounds__(kWinThreads, 1) attn_win_kernel(const __grid_constant__ WinArgs<D> a)
-{
-    using W = WinShape<D>;
-    constexpr int R = 8 * NT;  // rows of a block (p.RB)
-    constexpr int CW = W::CW;
-    extern __shared__ uint8_t smem_raw[];
-    WinSmem<D, NT> &sm = *reinterpret_cast<WinSmem<D, NT> *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const WinParams &p = a.p;
+    constexpr int NT = R == 16 ? 2 : 1;  // tiles of 8 rows of the score product
+    constexpr bool kMmaPv = R == 16;
+    constexpr int kStages = win_stages(R);
+    using Smem = WinSmem<D, R>;
+    constexpr int kTeam = Smem::kTeam, kTeams = Smem::kTeams;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const float NEG_INF = -__int_as_float(0x7f800000);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int team = warp / kTeam, slice = warp % kTeam;  // slice: this warp's 128 dims
+    const int g = lane >> 2, t = lane & 3;                // mma fragment coordinates
     const int C = p.whole, rank = blockIdx.x % C;
     int u = blockIdx.x / C;
-    Piece pc;
-    pc.it.b = u % p.n_rblk;
+    const int b = u % p.n_rblk;
     u /= p.n_rblk;
-    pc.it.kh = u % p.Hkv;
-    pc.it.s = u / p.Hkv;
-    const int s = pc.it.s, kh = pc.it.kh, m0 = pc.it.b * R, n_rows = min(p.M - m0, R);
+    const int kh = u % p.Hkv, s = u / p.Hkv;
+    const int m0 = b * R, n_rows = min(p.M - m0, R);
     allow_dependent_launch();
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < W::NU; ++k) {
-            mbar_init(&sm.full[k], 1);
-            mbar_init(&sm.empty[k], W::kGroups);
-        }
-        sm.abort_flag = 0;
-        sm.wait_limit = p.wait_limit;
-        fence_mbar_init();
-    }
-    if (warp == kConsumers && lane < W::kHeights) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.kmap[lane])) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.vmap[lane])) : "memory");
-    }
     wait_prior_grid();
-    __syncthreads();
 
     const int len = __ldg(p.lens + s);
     // output (and query) row of the block's row r
@@ -319,282 +188,383 @@ __global__ void __launch_bounds__(kWinThreads, 1) attn_win_kernel(const __grid_c
         }
         return;  // (the whole cluster)
     }
-    pc.it.len = len;
-    set_window(p, pc.it);  // len and everything below in squeezed positions
-    const int lim = block_lim(p, len, pc.it.b);
-    const int n_tiles = (lim + W::T - 1) / W::T;
-    pc.t0 = piece_start(n_tiles, rank, C);
-    pc.t1 = piece_start(n_tiles, rank + 1, C);
+    // the positions that some row sees: [0, sink_end) and [start, lim), as
+    // indexes [0, n)
+    const int first = block_start(p, len, b);
+    const int sink_end = first > p.sinks ? p.sinks : 0;
+    const int start = first > p.sinks ? first : 0;
+    const int lim = row_lim(p, len, m0 + R - 1);
+    const int n = sink_end + lim - start;
+    const int n_chunks = (n + kChunk - 1) / kChunk;
+    const int shift = start - sink_end;  // position of index i >= sink_end: i + shift
+    const int32_t *trow = p.table + (int64_t)s * p.table_stride;
 
-    const int slice = warp % W::kSlices, group = warp / W::kSlices;
-    const int g = lane >> 2, t = lane & 3;  // mma fragment coordinates
-    // o[4 c + k][y][2 d + e]: dim 64 c + 8 g + 2 k + d of row 8 y + 2 t + e
-    float o[8][NT][4];
-    float mref[NT][2], l[NT][2];
-    if (warp == kConsumers) {
-        if (pc.t0 < pc.t1)
-            win_producer<D, NT>(a, sm, pc, lane);
-    } else {
-        // the block's query rows 8 y + g, in the layout of K's
-        uint4 qf[NT][4];
+    // the pool row of index 16 ch + (lane % 16), or -1
+    auto lookup = [&](int ch) {
+        const int i = ch * kChunk + (lane & 15);
+        if (ch >= n_chunks || i >= n)
+            return -1;
+        const int pos = i < sink_end ? i : i + shift;
+        // pos / P: the product is short by at most one
+        int lp = (int)__umulhi((uint32_t)pos, p.page_inv), slot = pos - lp * p.P;
+        if (slot >= p.P) {
+            ++lp;
+            slot -= p.P;
+        }
+        const int page = __ldg(trow + lp);
+        if (page < 0 || page >= p.n_pages) {
+            set_flag(p.flags, kDevBadPage);
+            return -1;  // never read
+        }
+        return (page * p.Hkv + kh) * p.P + slot;
+    };
+    // K rows g and g + 8 of a chunk: dims 32 c + 8 t .. + 7 of the slice, copy
+    // 4 h + c
+    const uint32_t ring = smem_addr(&sm.ring[warp][0][0][0][lane]);
+    constexpr uint32_t kHalf = 8 * 32 * 16;  // bytes of a stage's K, or V
+    auto copy_k = [&](int rows, int stage) {
 #pragma unroll
-        for (int y = 0; y < NT; ++y) {
-            const bool there = g + 8 * y < n_rows;
-            const uint4 *src =
-                reinterpret_cast<const uint4 *>(p.q + (there ? row_of(g + 8 * y) : 0) * D + slice * 128 + 8 * t);
+        for (int h = 0; h < 2; ++h) {
+            const int r = __shfl_sync(0xffffffffu, rows, g + 8 * h);
+            const __nv_bfloat16 *src = p.k_pool + (int64_t)max(r, 0) * D + slice * 128 + 8 * t;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                qf[y][c] = there ? __ldg(src + 4 * c) : make_uint4(0, 0, 0, 0);
+                copy16(ring + stage * 2 * kHalf + (4 * h + c) * 512, src + 32 * c, r >= 0);
         }
-        // one past the last position that row 8 y + 2 t + e sees
-        int end[NT][2];
+        copies_commit();
+    };
+    // V of a chunk: rows, half a warp to a row; or fragments as K's, rows 2t, 2t +
+    // 1, 2t + 8, 2t + 9, dims 64 c + 8 g .. + 7 of the slice, copy 4 c + h
+    const int up = lane >> 4, q16 = lane & 15;
+    auto copy_v = [&](int rows, int stage) {
+        const uint32_t dst = ring + (stage * 2 + 1) * kHalf;
+        if constexpr (kMmaPv) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int r = __shfl_sync(0xffffffffu, rows, 2 * t + (h & 1) + (h >> 1) * 8);
+                const __nv_bfloat16 *src = p.v_pool + (int64_t)max(r, 0) * D + slice * 128 + 8 * g;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    copy16(dst + (4 * c + h) * 512, src + 64 * c, r >= 0);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = __shfl_sync(0xffffffffu, rows, 2 * k + up);
+                copy16(dst + k * 512, p.v_pool + (int64_t)max(r, 0) * D + slice * 128 + 8 * q16, r >= 0);
+            }
+        }
+        copies_commit();
+    };
+    const uint4(*const frag)[2][8][32] = sm.ring[warp];
+
+    const int step = C * kTeams;
+    int ch = rank * kTeams + team;
+    {
+        int rows[kStages];
+#pragma unroll
+        for (int k = 0; k < kStages; ++k)
+            rows[k] = lookup(ch + k * step);
+#pragma unroll
+        for (int k = 0; k < kStages; ++k) {
+            copy_k(rows[k], k);
+            copy_v(rows[k], k);
+        }
+    }
+    int rows_next = lookup(ch + kStages * step);
+    // the block's query rows 8 y + g, in the layout of K's
+    uint4 qf[NT][4];
+#pragma unroll
+    for (int y = 0; y < NT; ++y) {
+        const bool there = g + 8 * y < n_rows;
+        const uint4 *src =
+            reinterpret_cast<const uint4 *>(p.q + (there ? row_of(g + 8 * y) : 0) * D + slice * 128 + 8 * t);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            qf[y][c] = there ? __ldg(src + 4 * c) : make_uint4(0, 0, 0, 0);
+    }
+    // one past the last position that row 8 y + 2 t + e sees
+    int end[NT][2];
+#pragma unroll
+    for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            end[y][e] = row_lim(p, len, m0 + 8 * y + 2 * t + e);
+    // positions every row of the block sees need no mask
+    const int all_end = row_lim(p, len, m0), all_begin = lim - p.window;
+
+    // FMAs: rows 2 k and 2 k + 1, dim 8 q16 + d of the slice, over the positions of
+    // the lane's half
+    float2 o[kMmaPv ? 1 : R / 2][8];
+    // mma.sync: om[4 c + k][y][2 d + e] is dim 64 c + 8 g + 2 k + d of row 8 y + 2 t + e
+    float om[kMmaPv ? 8 : 1][NT][4];
+#pragma unroll
+    for (int k = 0; k < (kMmaPv ? 1 : R / 2); ++k)
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+            o[k][d] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < (kMmaPv ? 8 : 1); ++k)
 #pragma unroll
         for (int y = 0; y < NT; ++y)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                end[y][e] = row_lim(p, pc.it.len, m0 + 8 * y + 2 * t + e);
-                mref[y][e] = NEG_INF;
-                l[y][e] = 0.f;
-            }
-        // chunks that every row of the block sees whole need no mask
-        const int all_end = row_lim(p, pc.it.len, m0), all_begin = lim - p.window;
+            for (int e = 0; e < 4; ++e)
+                om[k][y][e] = 0.f;
+    float mref[NT][2], l[NT][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+    for (int y = 0; y < NT; ++y)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mref[y][e] = NEG_INF;
+            l[y][e] = 0.f;
+        }
+
+    int stage = 0;
+    for (int it = 0; ch < n_chunks; ch += step, ++it, stage = stage + 1 < kStages ? stage + 1 : 0) {
+        // ---- S^T = K Q^T: x[y][2 h + e] is index 16 ch + 8 h + g, row 8 y + 2 t + e
+        float x[NT][4];
+        copies_wait<2 * kStages - 1>();  // (K and V of each later chunk, this one's V)
+        {
+            uint4 k[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    k[h][c] = frag[stage][0][4 * h + c][lane];
+            // two chains of sums per tile
+            float z[NT][2][4];
+#pragma unroll
+            for (int y = 0; y < NT; ++y)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[y][f][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int y = 0; y < NT; ++y) {
+                    mma16816(z[y][0], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, qf[y][c].x, qf[y][c].y);
+                    mma16816(z[y][1], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, qf[y][c].z, qf[y][c].w);
+                }
 #pragma unroll
             for (int y = 0; y < NT; ++y)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[k][y][e] = 0.f;
-
-        // K: the lane's rows are positions pk and pk + 8 of a chunk (A's rows g and
-        // g + 8), V: positions 2 t and pv of each half (A's columns 2 t and 2 t + 1):
-        // A's odd rows are positions shifted by 4, so that eight lanes' 16 bytes
-        // lie on different banks
-        const int pk = g & 1 ? g ^ 4 : g, pv = (2 * t + 1) ^ 4;
-        bool ok = true;
-        uint32_t U = 0;  // first unit of the tile
-        for (int tile = pc.t0; ok && tile < pc.t1; ++tile, U += 2 * W::kSlices) {
-            const int p0 = tile * W::T + group * CW * kChunk;  // the warp's first position
-            // ---- S^T = K Q^T: x[i][y][2 h + e] is position p0 + 16 i + 8 h + pk, row 8 y + 2 t + e
-            float x[CW][NT][4];
-            {
-                const uint32_t uk = U + slice;
-                const int st = (int)(uk % W::NU);
-                ok = pwait(sm, &sm.full[st], (uk / W::NU) & 1u, p.flags, kWaitFull);
-                const uint8_t *kt = sm.ring[st] + (group * CW * kChunk + pk) * 128;
+                    x[y][e] = z[y][0][e] + z[y][1][e];
+        }
+        const int rows = rows_next;      // of the chunk kStages on
+        copy_k(rows, stage);
+        rows_next = lookup(ch + (kStages + 1) * step);
+        if constexpr (kTeam > 1) {
+            // sum over the team's slices, in one order for all of its warps
+            auto &xs = sm.s[it & 1];
 #pragma unroll
-                for (int i = 0; i < CW; ++i) {
-                    uint4 k[2][4];
+            for (int y = 0; y < NT; ++y)
+                *reinterpret_cast<float4 *>(&xs[warp][lane][4 * y]) =
+                    make_float4(x[y][0], x[y][1], x[y][2], x[y][3]);
+            named_barrier(1 + team, 32 * kTeam);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+            for (int y = 0; y < NT; ++y) {
+                float4 a = *reinterpret_cast<const float4 *>(&xs[team * kTeam][lane][4 * y]);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            k[h][c] = *reinterpret_cast<const uint4 *>(kt + (c >> 1) * W::kBox + (16 * i + 8 * h) * 128 +
-                                                                       (((4 * (c & 1) + t) ^ pk) << 4));
-                    // two chains of sums per tile of rows
-                    float z[NT][2][4];
+                for (int w = 1; w < kTeam; ++w) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&xs[team * kTeam + w][lane][4 * y]);
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
+                }
+                x[y][0] = a.x;
+                x[y][1] = a.y;
+                x[y][2] = a.z;
+                x[y][3] = a.w;
+            }
+        }
+        // ---- masked scores in log2 units; does some row's maximum grow too far?
+        const int i0 = ch * kChunk;
+        const int p0 = i0 < sink_end ? i0 : i0 + shift;
+        const bool one_run = i0 + kChunk <= sink_end || i0 >= sink_end;
+        const bool whole = one_run && i0 + kChunk <= n && p0 + kChunk <= all_end &&
+                           (p0 >= all_begin || p0 + kChunk <= p.sinks);
+        bool grow = false;
 #pragma unroll
-                    for (int y = 0; y < NT; ++y)
+        for (int y = 0; y < NT; ++y) {
 #pragma unroll
-                        for (int f = 0; f < 2; ++f)
+            for (int e = 0; e < 4; ++e) {
+                float v = x[y][e] * p.scale_log2;
+                if (!whole) {
+                    const int i = i0 + g + 8 * (e >> 1);
+                    const int pos = i < sink_end ? i : i + shift;
+                    if (i >= n || pos >= end[y][e & 1] ||
+                        (pos < end[y][e & 1] - p.window && pos >= p.sinks))
+                        v = NEG_INF;
+                }
+                x[y][e] = v;
+                grow = grow || v > mref[y][e & 1] + kRescaleLog2;
+            }
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                z[y][f][e] = 0.f;
+            for (int y = 0; y < NT; ++y) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(x[y][e], x[y][2 + e]);
 #pragma unroll
-                        for (int y = 0; y < NT; ++y) {
-                            mma16816(z[y][0], k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, qf[y][c].x, qf[y][c].y);
-                            mma16816(z[y][1], k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, qf[y][c].z, qf[y][c].w);
+                    for (int k = 4; k < 32; k <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                    const float m_new = fmaxf(mref[y][e], mx);
+                    const float al = mref[y][e] == NEG_INF ? 0.f : fast_exp2(mref[y][e] - m_new);
+                    mref[y][e] = m_new;
+                    l[y][e] *= al;
+                    if constexpr (kMmaPv) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            om[k][y][e] *= al;
+                            om[k][y][2 + e] *= al;
                         }
+                    } else if (g == 0 && 2 * t + e < R) {
+                        sm.alpha[warp][2 * t + e] = al;
+                    }
+                }
+            }
+            if constexpr (!kMmaPv) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < R / 2; ++k) {
+                    const float2 al = *reinterpret_cast<const float2 *>(&sm.alpha[warp][2 * k]);
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+                        o[k][d] = __fmul2_rn(o[k][d], al);
+                }
+            }
+        }
+        // ---- P: by position in shared memory, or in three parts in fragments:
+        // part[y][h][f] holds positions 8 h + 2 t and + 1 of row 8 y + g
+        uint32_t part[kMmaPv ? NT : 1][2][3];
+#pragma unroll
+        for (int y = 0; y < NT; ++y) {
+            const float n0 = mref[y][0] == NEG_INF ? 0.f : -mref[y][0];
+            const float n1 = mref[y][1] == NEG_INF ? 0.f : -mref[y][1];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 pr = make_float2(fast_exp2(x[y][2 * h] + n0), fast_exp2(x[y][2 * h + 1] + n1));
+                l[y][0] += pr.x;
+                l[y][1] += pr.y;
+                if constexpr (kMmaPv) {
+                    split3(pr.x, pr.y, part[y][h]);
+#pragma unroll
+                    for (int f = 0; f < 3; ++f)
+                        part[y][h][f] = transpose8(part[y][h][f]);
+                } else if (R > 4 || t < 2) {
+                    *reinterpret_cast<float2 *>(&sm.p[warp][8 * h + g][2 * t]) = pr;
+                }
+            }
+        }
+        // ---- O += P V (rows that were not read are zeros)
+        copies_wait<2 * kStages - 1>();
+        if constexpr (kMmaPv) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint4 v[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    v[h] = frag[stage][1][4 * c + h][lane];
+                float acc[4][NT][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int y = 0; y < NT; ++y)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            x[i][y][e] = z[y][0][e] + z[y][1][e];
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm.empty[st]);
-            }
-            if constexpr (W::kSlices > 1) {
-                // sum over the slices, in one order for all of the group's warps
-                auto &xs = sm.s[tile & 1];
+                            acc[k][y][e] = 0.f;
 #pragma unroll
-                for (int i = 0; i < CW; ++i)
+                for (int f = 2; f >= 0; --f) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // (dims 2 k and 2 k + 1 of the lane's eight, by pairs of positions)
+                        const uint32_t v0 = (&v[0].x)[k], v1 = (&v[1].x)[k], v2 = (&v[2].x)[k], v3 = (&v[3].x)[k];
+                        const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+                        const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+#pragma unroll
+                        for (int y = 0; y < NT; ++y)
+                            mma16816(acc[k][y], a0, a1, a2, a3, part[y][0][f], part[y][1][f]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int y = 0; y < NT; ++y)
-                        *reinterpret_cast<float4 *>(&xs[warp][i][lane][4 * y]) =
-                            make_float4(x[i][y][0], x[i][y][1], x[i][y][2], x[i][y][3]);
-                named_barrier(1 + group, 32 * W::kSlices);
 #pragma unroll
-                for (int i = 0; i < CW; ++i)
-#pragma unroll
-                    for (int y = 0; y < NT; ++y) {
-                        float4 b = *reinterpret_cast<const float4 *>(&xs[group * W::kSlices][i][lane][4 * y]);
-#pragma unroll
-                        for (int w = 1; w < W::kSlices; ++w) {
-                            const float4 v =
-                                *reinterpret_cast<const float4 *>(&xs[group * W::kSlices + w][i][lane][4 * y]);
-                            b.x += v.x;
-                            b.y += v.y;
-                            b.z += v.z;
-                            b.w += v.w;
-                        }
-                        x[i][y][0] = b.x;
-                        x[i][y][1] = b.y;
-                        x[i][y][2] = b.z;
-                        x[i][y][3] = b.w;
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            om[4 * c + k][y][e] += acc[k][y][e];
             }
-            // ---- masked scores in log2 units; does some row's maximum grow too far?
-            const bool whole = p0 + CW * kChunk <= all_end && (p0 >= all_begin || p0 + CW * kChunk <= p.sinks);
-            bool grow = false;
-#pragma unroll
-            for (int i = 0; i < CW; ++i)
-#pragma unroll
-                for (int y = 0; y < NT; ++y)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = x[i][y][e] * p.scale_log2;
-                        if (!whole) {
-                            // (positions that were not loaded are seen by no row)
-                            const int pos = p0 + 16 * i + 8 * (e >> 1) + pk, n = end[y][e & 1];
-                            if (pos >= n || (pos < n - p.window && pos >= p.sinks))
-                                v = NEG_INF;
-                        }
-                        x[i][y][e] = v;
-                        grow = grow || v > mref[y][e & 1] + kRescaleLog2;
-                    }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int y = 0; y < NT; ++y) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = NEG_INF;
-#pragma unroll
-                        for (int i = 0; i < CW; ++i)
-                            mx = fmax3(mx, x[i][y][e], x[i][y][2 + e]);
-#pragma unroll
-                        for (int k = 4; k < 32; k <<= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-                        const float m_new = fmaxf(mref[y][e], mx);
-                        const float alpha = mref[y][e] == NEG_INF ? 0.f : fast_exp2(mref[y][e] - m_new);
-                        mref[y][e] = m_new;
-                        l[y][e] *= alpha;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            o[k][y][e] *= alpha;
-                            o[k][y][2 + e] *= alpha;
-                        }
-                    }
-                }
-            }
-            const uint32_t uv = U + W::kSlices + slice;
-            const int st = (int)(uv % W::NU);
-            const uint8_t *vt = sm.ring[st] + group * CW * kChunk * 128;
-#pragma unroll
-            for (int i = 0; i < CW; ++i) {
-                // ---- P^T in three parts: part[y][f][h] holds A's columns 2 t, 2 t + 1 of half h, row 8 y + g
-                uint32_t part[NT][3][2];
-#pragma unroll
-                for (int y = 0; y < NT; ++y) {
-                    const float n0 = mref[y][0] == NEG_INF ? 0.f : -mref[y][0];
-                    const float n1 = mref[y][1] == NEG_INF ? 0.f : -mref[y][1];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float a0 = fast_exp2(x[i][y][2 * h] + n0), a1 = fast_exp2(x[i][y][2 * h + 1] + n1);
-                        l[y][0] += a0;
-                        l[y][1] += a1;
-                        split3(a0, a1, part[y][0][h], part[y][1][h], part[y][2][h]);
-#pragma unroll
-                        for (int f = 0; f < 3; ++f)
-                            part[y][f][h] = transpose8(part[y][f][h]);
-                    }
-                }
-                // ---- O^T += V^T P^T
-                if (i == 0)
-                    ok = pwait(sm, &sm.full[st], (uv / W::NU) & 1u, p.flags, kWaitFull) && ok;
-                // rows that were not loaded hold anything (0 * NaN = NaN)
-                bool there[4];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int pos = p0 + 16 * i + 8 * (h >> 1) + (h & 1 ? pv : 2 * t);
-                    there[h] = whole || (pos < pc.it.len && (pos < pc.it.sink_end || pos >= pc.it.dead_end));
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int r = h & 1 ? pv : 2 * t;
-                        v[h] = *reinterpret_cast<const uint4 *>(vt + c * W::kBox + (16 * i + 8 * (h >> 1) + r) * 128 +
-                                                                ((g ^ r) << 4));
-                        if (!whole && !there[h])
-                            v[h] = make_uint4(0, 0, 0, 0);
-                    }
-                    float acc[4][NT][4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int y = 0; y < NT; ++y)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[k][y][e] = 0.f;
-#pragma unroll
-                    for (int f = 2; f >= 0; --f) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            // (dims 2 k and 2 k + 1 of the lane's eight, by pairs of positions)
-                            const uint32_t v0 = (&v[0].x)[k], v1 = (&v[1].x)[k], v2 = (&v[2].x)[k], v3 = (&v[3].x)[k];
-                            const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
-                            const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
-#pragma unroll
-                            for (int y = 0; y < NT; ++y)
-                                mma16816(acc[k][y], a0, a1, a2, a3, part[y][f][0], part[y][f][1]);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int y = 0; y < NT; ++y)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[4 * c + k][y][e] += acc[k][y][e];
-                }
-            }
+        } else {
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.empty[st]);
+            const uint4 *const v_rows = &frag[stage][1][0][lane];
+#pragma unroll
+            for (int i = 0; i < kChunk / 2; ++i) {
+                const uint4 w = v_rows[i * 32];
+                const float v[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y),
+                                    bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
+#pragma unroll
+                for (int k = 0; k < R / 4; ++k) {
+                    const float4 pr = *reinterpret_cast<const float4 *>(&sm.p[warp][2 * i + up][4 * k]);
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) {
+                        const float2 vv = make_float2(v[d], v[d]);
+                        o[2 * k][d] = __ffma2_rn(make_float2(pr.x, pr.y), vv, o[2 * k][d]);
+                        o[2 * k + 1][d] = __ffma2_rn(make_float2(pr.z, pr.w), vv, o[2 * k + 1][d]);
+                    }
+                }
+            }
+            __syncwarp();  // (every lane read the chunk's V and P)
         }
+        copy_v(rows, stage);
     }
 
-    // ---- join: O by warp, maxima and sums by group ------------------------------
-    __syncthreads();  // every unit was consumed: the ring is free
-    if (warp < kConsumers) {
-        float(*const o_part)[128] = reinterpret_cast<float(*)[128]>(&sm.ring[0][0] + warp * R * 512);
+    copies_wait<0>();
+    __syncwarp();
+    float(*const o_part)[128] = reinterpret_cast<float(*)[128]>(&sm.ring[warp][0][0][0][0]);
+    // ---- join: O by warp, maxima and sums by team --------------------------------
 #pragma unroll
-        for (int y = 0; y < NT; ++y) {
+    for (int y = 0; y < NT; ++y) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int k = 4; k < 32; k <<= 1)
-                    l[y][e] += __shfl_xor_sync(0xffffffffu, l[y][e], k);
-                const int r = 8 * y + 2 * t + e;
-                if (slice == 0 && g == 0) {
-                    sm.m[group][r] = mref[y][e];
-                    sm.l[group][r] = l[y][e];
-                }
-                if (r < n_rows) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int k = 0; k < 4; k += 2)
-                            *reinterpret_cast<float4 *>(&o_part[r][64 * c + 8 * g + 2 * k]) =
-                                make_float4(o[4 * c + k][y][e], o[4 * c + k][y][2 + e], o[4 * c + k + 1][y][e],
-                                            o[4 * c + k + 1][y][2 + e]);
-                }
+            for (int k = 4; k < 32; k <<= 1)
+                l[y][e] += __shfl_xor_sync(0xffffffffu, l[y][e], k);
+            const int r = 8 * y + 2 * t + e;
+            if (slice == 0 && g == 0 && r < R) {
+                sm.m[team][r] = mref[y][e];
+                sm.l[team][r] = l[y][e];
             }
+        }
+    }
+    if constexpr (kMmaPv) {
+#pragma unroll
+        for (int y = 0; y < NT; ++y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2)
+                        *reinterpret_cast<float4 *>(&o_part[8 * y + 2 * t + e][64 * c + 8 * g + 2 * k]) =
+                            make_float4(om[4 * c + k][y][e], om[4 * c + k][y][2 + e], om[4 * c + k + 1][y][e],
+                                        om[4 * c + k + 1][y][2 + e]);
+    } else {
+        // the lower half of the warp ends up with the even rows, the upper with the odd
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k) {
+            float sum[8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                sum[d] = (up ? o[k][d].y : o[k][d].x) +
+                         __shfl_xor_sync(0xffffffffu, up ? o[k][d].x : o[k][d].y, 16);
+            float4 *dst = reinterpret_cast<float4 *>(&o_part[2 * k + up][8 * q16]);
+            dst[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            dst[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
         }
     }
     cluster_sync();
@@ -604,18 +574,19 @@ __global__ void __launch_bounds__(kWinThreads, 1) attn_win_kernel(const __grid_c
         float top = NEG_INF;
         for (int k = 0; k < C; ++k)
 #pragma unroll
-            for (int w = 0; w < W::kGroups; ++w)
+            for (int w = 0; w < kTeams; ++w)
                 top = fmaxf(top, peer_f32(peer_addr(m_addr, k) + (w * R + r) * 4));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.f;
         for (int k = 0; k < C; ++k) {
 #pragma unroll
-            for (int w = 0; w < W::kGroups; ++w) {
+            for (int w = 0; w < kTeams; ++w) {
                 const uint32_t at = (w * R + r) * 4;
-                // (a group without positions: 2^-inf = 0)
+                // (a team without positions: 2^-inf = 0)
                 const float wt = fast_exp2(peer_f32(peer_addr(m_addr, k) + at) - top);
                 sum = fmaf(wt, peer_f32(peer_addr(l_addr, k) + at), sum);
-                const float4 v = peer_f32x4(peer_addr(o_addr, k) + (w * W::kSlices + d / 128) * R * 512 +
+                const float4 v = peer_f32x4(peer_addr(o_addr, k) +
+                                            (uint32_t)((w * kTeam + d / 128) * sizeof(sm.ring[0])) +
                                             (r * 128 + d % 128) * 4);
                 acc.x = fmaf(wt, v.x, acc.x);
                 acc.y = fmaf(wt, v.y, acc.y);
@@ -653,7 +624,7 @@ struct WinLaunch {
 };
 
 // Clusters of C blocks the current device holds at once (asked once per device).
-template <int D, int NT>
+template <int D, int R>
 int win_clusters(int C)
 {
     static std::atomic<int> known[kMaxDevices][kMaxCluster + 1];
@@ -662,71 +633,70 @@ int win_clusters(int C)
         return 0;
     int n = known[dev][C].load(std::memory_order_relaxed);
     if (n == 0) {
-        constexpr size_t bytes = win_smem_bytes<D, NT>();
+        constexpr size_t bytes = sizeof(WinSmem<D, R>);
         static std::atomic<bool> configured[kMaxDevices];
-        if (set_smem_limit_once(attn_win_kernel<D, NT>, bytes, configured) != cudaSuccess)
+        if (set_smem_limit_once(attn_win_kernel<D, R>, bytes, configured) != cudaSuccess)
             return 0;
         WinLaunch launch(C, C, bytes, nullptr);
         launch.cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, attn_win_kernel<D, NT>, &launch.cfg) != cudaSuccess)
+        if (cudaOccupancyMaxActiveClusters(&n, attn_win_kernel<D, R>, &launch.cfg) != cudaSuccess)
             return 0;
         known[dev][C].store(n, std::memory_order_relaxed);
     }
     return n;
 }
 
-template <int D, int NT>
+template <int D, int R>
 cudaError_t launch_win(const WinParams &p, int grid, cudaStream_t stream)
 {
-    constexpr size_t bytes = win_smem_bytes<D, NT>();
-    static_assert(bytes <= 232448, "shared memory");
+    constexpr size_t bytes = sizeof(WinSmem<D, R>);
+    static_assert(win_blocks(R) * (bytes + 1024) <= 228 * 1024, "shared memory");
     static std::atomic<bool> configured[kMaxDevices];
-    const cudaError_t e = set_smem_limit_once(attn_win_kernel<D, NT>, bytes, configured);
+    const cudaError_t e = set_smem_limit_once(attn_win_kernel<D, R>, bytes, configured);
     if (e != cudaSuccess)
         return e;
-    WinArgs<D> a;
-    a.p = p;
-    for (int h = 0; h < WinShape<D>::kHeights; ++h)
-        if (!make_pool_map(&a.kmap[h], p.k_pool, p, 1 << h) || !make_pool_map(&a.vmap[h], p.v_pool, p, 1 << h))
-            return cudaErrorInvalidValue;
     WinLaunch launch(p.whole, grid, bytes, stream);
-    return cudaLaunchKernelEx(&launch.cfg, attn_win_kernel<D, NT>, a);
+    return cudaLaunchKernelEx(&launch.cfg, attn_win_kernel<D, R>, p);
 }
 
-template <int NT>
+template <int R>
 cudaError_t launch_win_rows(const WinParams &p, int grid, cudaStream_t stream)
 {
-    return p.D == 128   ? launch_win<128, NT>(p, grid, stream)
-           : p.D == 256 ? launch_win<256, NT>(p, grid, stream)
-                        : launch_win<512, NT>(p, grid, stream);
+    return p.D == 128   ? launch_win<128, R>(p, grid, stream)
+           : p.D == 256 ? launch_win<256, R>(p, grid, stream)
+                        : launch_win<512, R>(p, grid, stream);
 }
 
-template <int NT>
+template <int R>
 int win_clusters_rows(int D, int C)
 {
-    return D == 128 ? win_clusters<128, NT>(C) : D == 256 ? win_clusters<256, NT>(C) : win_clusters<512, NT>(C);
+    return D == 128 ? win_clusters<128, R>(C) : D == 256 ? win_clusters<256, R>(C) : win_clusters<512, R>(C);
 }
 
 }  // namespace
 
 // Blocks per cluster.  The blocks of one wave run side by side; a block's
-// time is its tiles one after another, plus starting and joining (about
-// kEntry tiles).  So: the cluster size whose waves times that is least (ties to
-// the smaller).
+// time is its warps' chunks one after another, plus starting and joining
+// (about kEntry chunks).  So: the cluster size whose waves times that is
+// least (ties to the smaller).  With 96 units, 3 blocks of 2 to an SM would be
+// 93 clusters at once and a second wave for three (68 us against 57 in
+// clusters of 2).
 int win_cluster_size(const WinParams &p, int64_t units)
 {
     constexpr int kEntry = 4;
     const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + p.W);
-    const int T = p.D == 512 ? 64 : 128;
-    const int64_t tiles = (seen + T - 1) / T;
+    const int64_t chunks = (seen + kChunk - 1) / kChunk;
+    const int teams = kWinWarps / (p.D / 128);
     int best = 1;
     int64_t least = INT64_MAX;
     for (int C = 1; C <= kMaxCluster; ++C) {
-        const int64_t at_once = p.RB == 8 ? win_clusters_rows<1>(p.D, C) : win_clusters_rows<2>(p.D, C);
+        const int64_t at_once = p.RB == 4   ? win_clusters_rows<4>(p.D, C)
+                                : p.RB == 8 ? win_clusters_rows<8>(p.D, C)
+                                            : win_clusters_rows<16>(p.D, C);
         if (at_once <= 0)
             continue;
         const int64_t waves = (units + at_once - 1) / at_once;
-        const int64_t cost = waves * ((tiles + C - 1) / C + kEntry);
+        const int64_t cost = waves * ((chunks + C * teams - 1) / (C * teams) + kEntry);
         if (cost < least) {
             least = cost;
             best = C;
@@ -737,7 +707,9 @@ int win_cluster_size(const WinParams &p, int64_t units)
 
 cudaError_t launch_attn_win(const WinParams &p, int grid, cudaStream_t stream)
 {
-    return p.RB == 8 ? launch_win_rows<1>(p, grid, stream) : launch_win_rows<2>(p, grid, stream);
+    return p.RB == 4   ? launch_win_rows<4>(p, grid, stream)
+           : p.RB == 8 ? launch_win_rows<8>(p, grid, stream)
+                       : launch_win_rows<16>(p, grid, stream);
 }
 
 }  // namespace tfp

@@ -74,6 +74,7 @@ struct AttnParams {
 // kernels carry none of it.
 struct WinParams : AttnParams {
     int32_t window, sinks;      // window >= 1, sinks >= 0, both at most max_len
+    uint32_t page_inv;          // floor(2^32 / P), at most 2^32 - 1
 };
 
 // Floats per partial slot: SR rows of O (D floats each), then SR running

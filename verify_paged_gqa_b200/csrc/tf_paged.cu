@@ -130,6 +130,7 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     p.P = pool->page_size;
     if (win) {
         // a window or sinks past every length see what max_len does
+        p.page_inv = p.P == 1 ? UINT32_MAX : (uint32_t)((1ull << 32) / p.P);
         p.window = win->window < st->max_len ? win->window : st->max_len;
         p.sinks = win->sinks < st->max_len ? win->sinks : st->max_len;
     }
@@ -184,7 +185,7 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
             return TF_EUNSUPPORTED;
         if (takes_win_kernel(p)) {
             plan->kernel = Kernel::kWin;
-            p.RB = M <= 8 ? 8 : 16;
+            p.RB = M <= 4 ? 4 : M <= 8 ? 8 : 16;
         } else if (nr > 0) {
             plan->kernel = Kernel::kPm;
             p.RB = nr;

@@ -675,20 +675,19 @@ int win_clusters_rows(int D, int C)
 
 }  // namespace
 
-// Blocks per cluster.  The blocks of one wave run side by side; a block's
-// time is its warps' chunks one after another, plus starting and joining
-// (about kEntry chunks).  So: the cluster size whose waves times that is
-// least (ties to the smaller).  With 96 units, 3 blocks of 2 to an SM would be
-// 93 clusters at once and a second wave for three (68 us against 57 in
-// clusters of 2).
-int win_cluster_size(const WinParams &p, int64_t units)
+// Blocks per cluster, and what the call then costs (in chunks).  The blocks of
+// one wave run side by side; a block's time is its warps' chunks one after
+// another, plus starting and joining (about kEntry chunks).  So: the cluster
+// size whose waves times that is least (ties to the smaller).  With 96 units
+// and two blocks to an SM, clusters of 3 were 93 at once and a second wave for
+// the other three (68 us against 57 in clusters of 2).
+WinSplit win_split(const WinParams &p, int64_t units)
 {
     constexpr int kEntry = 4;
     const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + p.W);
     const int64_t chunks = (seen + kChunk - 1) / kChunk;
     const int teams = kWinWarps / (p.D / 128);
-    int best = 1;
-    int64_t least = INT64_MAX;
+    WinSplit best = {1, INT64_MAX};
     for (int C = 1; C <= kMaxCluster; ++C) {
         const int64_t at_once = p.RB == 4   ? win_clusters_rows<4>(p.D, C)
                                 : p.RB == 8 ? win_clusters_rows<8>(p.D, C)
@@ -697,10 +696,8 @@ int win_cluster_size(const WinParams &p, int64_t units)
             continue;
         const int64_t waves = (units + at_once - 1) / at_once;
         const int64_t cost = waves * ((chunks + C * teams - 1) / (C * teams) + kEntry);
-        if (cost < least) {
-            least = cost;
-            best = C;
-        }
+        if (cost < best.cost)
+            best = {C, cost};
     }
     return best;
 }

@@ -142,11 +142,14 @@ cudaError_t launch_pages_move(MoveParams p, int sms, cudaStream_t stream);
 // Rows per row block of the CUDA-core partial kernel.
 constexpr int kSimtRows = 4;
 
-// Sliding-window kernel of row blocks of 8 or 16 rows (attn_win.cu): grid =
-// units * p.whole blocks in clusters of p.whole = win_cluster_size, one per
-// unit.
+// Sliding-window kernel of row blocks of 4, 8 or 16 rows (attn_win.cu): grid =
+// units * p.whole blocks in clusters of p.whole = win_split's C, one per unit.
 constexpr int kMaxCluster = 8;
-int win_cluster_size(const WinParams &p, int64_t units);
+struct WinSplit {
+    int C;
+    int64_t cost;  // in chunks of 16 positions, one after another
+};
+WinSplit win_split(const WinParams &p, int64_t units);
 cudaError_t launch_attn_win(const WinParams &p, int grid, cudaStream_t stream);
 
 template <int D>

@@ -106,8 +106,41 @@ bool pool_rows_past_31_bits(const tf_kv_pool *pool)
     return (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size > INT32_MAX;
 }
 
-// Blocks of up to 16 rows take the cluster kernel (attn_win.cu).
-bool takes_win_kernel(const WinParams &p) { return p.M <= 16; }
+// Row blocks of the position-major or prompt kernel against the cluster kernel
+// (attn_win.cu) for a sliding-window call, by estimates fitted to both kernels
+// over 475 calls (head dims 128, 256 and 512; 8 to 1,600 rows per KV head; 2 to
+// 256 units; windows of 64 to 8,192): the choice is 0.7% slower than the faster
+// of the two in the geometric mean, 27% at worst, where always the cluster
+// kernel up to 16 rows was 21%, never 39%.  In tenths of microseconds:
+//   cluster      its chunks one after another, 1.4 to 2.0 us each: it starts in
+//                about 4 us, but reads the unit again for every 16 rows, and
+//                its products run on mma.sync and FMAs
+//   tensor core  18 to 28 us to start and merge, then 1.6, 2.6 or 4.6 us per
+//                128-position tile, and 6 to 14 per unit
+// Sets p.RB and p.whole for the cluster kernel when it is taken.
+bool takes_win_kernel(WinParams &p, int sms)
+{
+    const int d = p.D == 128 ? 0 : p.D == 256 ? 1 : 2;
+    WinParams c = p;
+    c.RB = p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;
+    const int64_t heads = (int64_t)p.S * p.Hkv;
+    const int64_t units = heads * ((p.M + c.RB - 1) / c.RB);
+    if (units > INT32_MAX / kMaxCluster)
+        return false;
+    const WinSplit split = win_split(c, units);
+    const int64_t cluster = split.cost < INT64_MAX / 64 ? split.cost * (c.RB <= 8 ? 14 + d : 16 + 2 * d) : INT64_MAX;
+    const int rows = p.D > 128 || p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;  // of its row blocks
+    const int64_t blocks = (p.M + rows - 1) / rows;
+    const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + std::min(p.W, (rows + p.G - 1) / p.G));
+    const int64_t tiles2 = 2 * ((seen + 127) / 128) + 1;  // (half a tile more for the edges)
+    constexpr int kStart[3] = {180, 210, 280}, kTile[3] = {16, 26, 46}, kUnit[3] = {60, 100, 140};
+    const int64_t tensor = kStart[d] + heads * blocks * (tiles2 * kTile[d] / 2 + kUnit[d]) / sms;
+    if (cluster >= tensor)
+        return false;
+    p.RB = c.RB;
+    p.whole = split.C;
+    return true;
+}
 
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
               int32_t rows_max, bool tree, Plan *plan, const Window *win = nullptr)
@@ -183,9 +216,12 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         const int nr = pm_rows(p);
         if (pool_rows_past_31_bits(pool))
             return TF_EUNSUPPORTED;
-        if (takes_win_kernel(p)) {
+        int sms = 0;
+        rc = device_sm_count(&sms);
+        if (rc != TF_OK)
+            return rc;
+        if (takes_win_kernel(p, sms)) {
             plan->kernel = Kernel::kWin;
-            p.RB = M <= 4 ? 4 : M <= 8 ? 8 : 16;
         } else if (nr > 0) {
             plan->kernel = Kernel::kPm;
             p.RB = nr;
@@ -246,7 +282,8 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     // than a few idle SMs (measured on the chunked prompt: 128 units on 148).
     const int64_t units = (int64_t)p.S * p.Hkv * p.n_rblk;
     const int cap = sms < kMaxCtas ? sms : kMaxCtas;
-    p.whole = plan->kernel == Kernel::kPrompt && units <= cap && 4 * units >= 3 * (int64_t)cap;
+    if (plan->kernel == Kernel::kPrompt)
+        p.whole = units <= cap && 4 * units >= 3 * (int64_t)cap;
     // A sliding-window call on the position-major kernel with fewer units than
     // CTAs: as many whole pieces per unit as there are CTAs for, if that uses
     // three quarters of them.
@@ -256,13 +293,10 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         if (4 * units * pieces >= 3 * (int64_t)cap || pieces == tiles)
             p.whole = static_cast<int32_t>(pieces);
     }
-    if (p.whole)
+    if (p.whole && plan->kernel != Kernel::kWin)
         grid = units > 0 ? units * p.whole : 1;
     plan->grid = static_cast<int>(grid);
     if (plan->kernel == Kernel::kWin) {
-        if (units > INT32_MAX / 8)
-            return TF_EINVAL;
-        p.whole = win_cluster_size(p, units);
         plan->grid = static_cast<int>(units * p.whole);
         plan->ws_bytes = kWsHeaderBytes;
         return TF_OK;

@@ -110,6 +110,7 @@ def test_prompt_chunks_of_wide_heads(d, rows):
 
 
 @pytest.mark.parametrize("rows,G,window,sinks,lens", [
+    (64, 8, 6000, 4, [14000, 6100]), (700, 4, 5000, 4, [12000]), (8, 8, 9000, 130, [30000, 9200, 9130]),
     (1, 4, 4096, 4, [40960, 9000, 4100, 17]), (1, 8, 8192, 64, [32768, 8192, 8256, 8257]),
     (8, 8, 2048, 4, [20000, 2055, 131072]), (512, 4, 1024, 4, [9216, 600]), (1, 4, 30000, 1000, [40000, 31001])])
 def test_long_contexts_over_many_cta_ranges(rows, G, window, sinks, lens):
@@ -136,11 +137,15 @@ def test_a_window_past_every_length_sees_the_whole_context(d, rows):
     assert torch.equal(a, c.call(window=1, sinks=c.max_len))
 
 
-@pytest.mark.parametrize("d,G,rows", [(128, 8, 8), (128, 4, 1), (256, 8, 3), (512, 4, 4), (128, 4, 100)])
-def test_growing_scores(d, G, rows):
+@pytest.mark.parametrize("d,G,rows,window,lens", [
+    (128, 8, 8, 900, [3000, 1308]), (128, 4, 1, 900, [3000, 1301]), (256, 8, 3, 900, [3000, 1303]), (512, 4, 4, 900, [3000, 1304]),
+    (128, 4, 100, 900, [3000, 1400]), (128, 1, 3, 900, [3000]), (128, 4, 4, 2000, [3000, 1304]),
+    # many tiles of one block: sums are folded, between and along with changes of reference
+    (128, 8, 8, 6000, [9000] * 60), (256, 8, 8, 3000, [5000] * 40), (512, 8, 8, 2500, [4000] * 40), (128, 4, 300, 5000, [8000] * 4)])
+def test_growing_scores(d, G, rows, window, lens):
     """K scaled up along the context: running maxima move many times."""
-    c = WindowCase([3000, 1300 + rows], rows, 900, 40, d=d, G=G, P=512, seed=rows + d)
-    for s in range(2):
+    c = WindowCase(lens, rows, window, 40, d=d, G=G, P=512, seed=rows + d)
+    for s in range(len(lens)):
         ramp = (1.0 + 14.0 * torch.arange(c.k[s].shape[0], device="cuda") / c.k[s].shape[0])[:, None, None]
         c.k[s] = (c.k[s].float() * ramp).to(torch.bfloat16)
         for j, page in enumerate(c.table[s].tolist()):

@@ -55,6 +55,12 @@ constexpr uint32_t kUnit = kRingUnit;    // one ring unit: 128 positions x 128 d
 constexpr float kRescaleLog2 = 8.f;      // move a row's reference max only past this growth
 constexpr uint32_t kSmemCap = 232448;    // dynamic shared memory per block
 
+// Tensor memory is allocated in powers of two.
+constexpr uint32_t tmem_cols(uint32_t n)
+{
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
+}
+
 template <int D, int NR>
 struct PmCfg {
     static constexpr int DB = D / 128;                         // units per K (or V) tile
@@ -64,8 +70,10 @@ struct PmCfg {
     static constexpr uint32_t kColS = 0;
     static constexpr uint32_t kColO = 2 * NR;
     static constexpr uint32_t kCols = 2 * NR + DB * 2 * NR;
-    static constexpr uint32_t kTmemCols =
-        kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static constexpr uint32_t kTmemCols = tmem_cols(kCols);
+    // sliding windows: DB blocks of NR columns that O^T is folded into
+    static constexpr uint32_t kColF = kCols;
+    static constexpr uint32_t kTmemColsWin = tmem_cols(kCols + DB * NR);
     static constexpr uint32_t kSmall = 48 * NR + 512;  // per-row arrays, range, barriers
     // P^T buffers: with one, the softmax of tile t + 1 stores P only after
     // PV(t) completed, and the shared memory goes to the K/V ring instead
@@ -81,7 +89,7 @@ struct PmCfg {
     static constexpr bool kDual = D == 128;
     static constexpr int NK = kDual ? 2 : NU;
     static constexpr int NV = kDual ? NU - 2 : NU;
-    static_assert(kCols <= 512, "tensor memory");
+    static_assert(kCols + DB * NR <= 512, "tensor memory");
     static_assert(NU >= 2 && (!kDual || NV >= 2), "ring");
     static_assert(NR == 32 || NR == 64, "row block");
     static constexpr int kSoftThreads = 4 * NR;        // 32 rows per softmax thread
@@ -261,7 +269,7 @@ __device__ __forceinline__ void pm_issuer(const A &a, PmSmem<D, NR> &sm)
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                     umma_f16(tmem + C::kColO + vb * 2 * NR, sw128_desc(va + s * 2048, kBox, 1024),
-                             sw128_desc(pb + s * 2048, kBox, 1024), idPV, (t > 0 || s > 0) ? 1u : 0u);
+                             sw128_desc(pb + s * 2048, kBox, 1024), idPV, (pv_adds(p, t) || s > 0) ? 1u : 0u);
                 umma_commit(&sm.empty[st]);
                 ++U;
             }
@@ -521,7 +529,7 @@ __device__ __forceinline__ void pm_pv_issuer(const A &a, PmSmem<D, NR> &sm, int 
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                     umma_f16(tmem + C::kColO + vb * 2 * NR, sw128_desc(va + s * 2048, kBox, 1024),
-                             sw128_desc(pb + s * 2048, kBox, 1024), idPV, (t > 0 || s > 0) ? 1u : 0u);
+                             sw128_desc(pb + s * 2048, kBox, 1024), idPV, (pv_adds(p, t) || s > 0) ? 1u : 0u);
                 umma_commit(&sm.empty[st]);
             }
             }
@@ -715,6 +723,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 mx = max_tree(x);
                 slow = block_any<NT>(mx > kRescaleLog2);
             }
+            bool moved = false;
             if (slow) {
                 // --- a new reference max for rows whose max grew past it ---
                 float y[32];
@@ -725,7 +734,6 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 xpose_reduce<32, true>(y, lane);
                 sm.red[wq][R0 + lane] = y[0];
                 named_barrier(1, NT);
-                bool moved = false;
                 if (st < NR) {
                     const float tmax = fmaxf(fmaxf(sm.red[0][st], sm.red[1][st]),
                                              fmaxf(sm.red[2][st], sm.red[3][st]));
@@ -739,7 +747,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                     moved = t > 0 && grow && m_old != NEG_INF;
                 }
                 moved = block_any<NT>(moved);  // also publishes mref / negm / alpha
-                if (moved) {
+                if (kMask != kWindow && moved) {
                     // PV(u - 1) must be done before O^T is touched; this warp
                     // rescales its rows' hi and lo columns of every dim block
                     ok = pwait(sm, &sm.o_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u, p.flags,
@@ -777,6 +785,53 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
 #pragma unroll
                     for (int r = 0; r < 32; ++r)
                         x[r] = pm_sees<kMask>(r, rvis, vis) ? x[r] : NEG_INF;
+                }
+            }
+            if constexpr (kMask == kWindow) {
+                // O^T joins the folded sums every kFoldTiles tiles; a moved
+                // reference rescales both
+                const bool fold = t > 0 && t % kFoldTiles == 0;
+                if (moved || fold) {
+                    ok = pwait(sm, &sm.o_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u, p.flags,
+                               kWaitEmpty) && ok;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < C::DB; ++c) {
+                        const uint32_t th = lane_base + C::kColO + c * 2 * NR + R0;
+                        const uint32_t tf = lane_base + C::kColF + c * NR + R0;
+                        uint32_t a[32], b[32];
+                        tmem_ld32(th, a);
+                        tmem_ld32(th + NR, b);
+                        tmem_wait_ld();
+                        if (fold) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                a[e] = __float_as_uint(__uint_as_float(a[e]) + __uint_as_float(b[e]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                a[e] = __float_as_uint(__uint_as_float(a[e]) * sm.alpha[R0 + e]);
+                                b[e] = __float_as_uint(__uint_as_float(b[e]) * sm.alpha[R0 + e]);
+                            }
+                            tmem_st32(th, a);
+                            tmem_st32(th + NR, b);
+                        }
+                        // folded sums exist from the first fold on
+                        if (t > kFoldTiles) {
+                            tmem_ld32(tf, b);
+                            tmem_wait_ld();
+                        }
+                        if (fold || t > kFoldTiles) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float f = (t > kFoldTiles ? __uint_as_float(b[e]) : 0.f) +
+                                                (fold ? __uint_as_float(a[e]) : 0.f);
+                                b[e] = __float_as_uint(moved ? f * sm.alpha[R0 + e] : f);
+                            }
+                            tmem_st32(tf, b);
+                        }
+                    }
+                    tmem_wait_st();
                 }
             }
             // --- V rows past the stream's end: zero them (0 * NaN = NaN) ----
@@ -880,6 +935,13 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
             tmem_ld32(lane_base + C::kColO + vb * 2 * NR + R0, hi);
             tmem_ld32(lane_base + C::kColO + vb * 2 * NR + NR + R0, lo);
             tmem_wait_ld();
+            if (kMask == kWindow && n > kFoldTiles) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    hi[e] = __float_as_uint(__uint_as_float(hi[e]) + __uint_as_float(lo[e]));
+                tmem_ld32(lane_base + C::kColF + vb * NR + R0, lo);
+                tmem_wait_ld();
+            }
             if (write) {
                 const int d = 128 * vb + tid;
 #pragma unroll
@@ -939,7 +1001,7 @@ __global__ void __launch_bounds__(PmCfg<D, NR>::kThreads, 1)
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(&sm.tmem_base)), "r"(C::kTmemCols)
+                         smem_addr(&sm.tmem_base)), "r"(kMask == kWindow ? C::kTmemColsWin : C::kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -983,7 +1045,7 @@ __global__ void __launch_bounds__(PmCfg<D, NR>::kThreads, 1)
     tc_fence_after();
     if (warp == 1) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem_base),
-                     "r"(C::kTmemCols)
+                     "r"(kMask == kWindow ? C::kTmemColsWin : C::kTmemCols)
                      : "memory");
     }
 }

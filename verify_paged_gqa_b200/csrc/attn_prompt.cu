@@ -48,7 +48,9 @@ constexpr int kThreads = 320;      // producer, issuer, 8 softmax warps
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kPAtom = 32768;     // P: [256 rows][64 positions] bf16, SW128 K-major
 constexpr uint32_t kPBytes = 2 * kPAtom;
-// tensor memory: S (128 columns), O^T (hi rows 128, lo rows 128), Q (64)
+constexpr uint32_t kPLo = 16 * 1024;   // P_lo rows in an atom, after the 128 P_hi rows
+// tensor memory: S (128 columns), O^T (hi rows 128, lo rows 128; under long
+// sliding windows 128 for both, then 128 that O^T is folded into), Q (64)
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = 128;
 constexpr uint32_t kColQ = 384;
@@ -117,14 +119,15 @@ __device__ __forceinline__ bool pr_qk(PrSmem &sm, uint32_t &U, uint32_t u, uint3
 }
 
 // One lane.  Per segment: QK(0), then per tile t: QK(t + 1), PV(t).
-template <class A>
+template <bool kFold, class A>
 __device__ __forceinline__ void pr_issuer(const A &a, PrSmem &sm)
 {
     const auto &p = a.p;
     const uint32_t tmem = sm.tmem_base;
     // O^T += V^T P^T: A = V^T (MN-major, from the V unit), B = P (K-major,
-    // [256 rows: hi then lo][positions]), N = 256
-    constexpr uint32_t idPV = f16_idesc(128, 2 * RR, 1, 0);
+    // [256 rows: hi then lo][positions]), N = 256; long windows add the two parts
+    // into the same 128 columns, one after the other
+    constexpr uint32_t idPV = f16_idesc(128, kFold ? RR : 2 * RR, 1, 0);
     const uint32_t ring0 = smem_addr(sm.ring[0]);
     const uint32_t pb = smem_addr(sm.pbuf);
 
@@ -161,11 +164,22 @@ __device__ __forceinline__ void pr_issuer(const A &a, PrSmem &sm)
             if (!ok)
                 break;
             const uint32_t va = ring0 + st * kRingUnit;
+            if constexpr (kFold) {
+                // (the small part first)
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-                umma_f16(tmem + kColO, sw128_desc(va + s * 2048, kRingBox, 1024),
-                         sw128_desc(pb + (s >> 2) * kPAtom + (s & 3) * 32, 16, 1024), idPV,
-                         (t > 0 || s > 0) ? 1u : 0u);
+                for (int f = 1; f >= 0; --f)
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        umma_f16(tmem + kColO, sw128_desc(va + s * 2048, kRingBox, 1024),
+                                 sw128_desc(pb + (s >> 2) * kPAtom + f * kPLo + (s & 3) * 32, 16, 1024), idPV,
+                                 (pv_adds(p, t) || s > 0 || f == 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    umma_f16(tmem + kColO, sw128_desc(va + s * 2048, kRingBox, 1024),
+                             sw128_desc(pb + (s >> 2) * kPAtom + (s & 3) * 32, 16, 1024), idPV,
+                             (t > 0 || s > 0) ? 1u : 0u);
+            }
             umma_commit(&sm.empty[st]);
             ++U;
             umma_commit(&sm.o_done);
@@ -191,7 +205,7 @@ __device__ __forceinline__ uint64_t low_bits(int n)
 // row's half; a row's two threads agree on the row's reference max (they
 // compute it from the same shared values).  In the epilogue the thread reads
 // O^T lane r (head dim r) for rows [64 hh, 64 hh + 64).
-template <bool kWin, class A>
+template <bool kWin, bool kFold, class A>
 __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int lane)
 {
     const auto &p = a.p;
@@ -205,7 +219,7 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
     // this row's lines of K-atom hh of the P tile: hi row r, lo row 128 + r
     uint8_t *const at = sm.pbuf + hh * kPAtom;
     const uint32_t phi = (uint32_t)((r >> 3) * 1024 + (r & 7) * 128);
-    const uint32_t plo = phi + 16 * 1024;
+    const uint32_t plo = phi + kPLo;
     const int sw = r & 7;
 
     SegCursor cur;
@@ -314,6 +328,7 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             const float hm = hmax == NEG_INF ? NEG_INF : hmax * sl;
             // a half that would move the row's reference calls for the slow path
             const bool hgrow = hm != NEG_INF && (mref == NEG_INF || hm > mref + kRescaleLog2);
+            bool moved = false;
             if (block_any<256>(hgrow)) {
                 // the row's tile max from its two halves; both threads of the
                 // row take the same decision from the same values
@@ -332,7 +347,8 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                     sm.alpha[r] = al;
                 // rows with an earlier reference moved: rescale their O^T
                 // columns (this warp: the hi columns for hh = 0, lo for hh = 1)
-                if (block_any<256>(grow && al != 0.f)) {
+                moved = block_any<256>(grow && al != 0.f);
+                if (!kFold && moved) {
                     ok = pwait(sm, &sm.o_done, (u - 1) & 1u, p.flags, kWaitEmpty) && ok;
                     tc_fence_after();
 #pragma unroll 1
@@ -345,6 +361,39 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                         for (int e = 0; e < 32; ++e)
                             v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.alpha[32 * c + e]);
                         tmem_st32(ta, v);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            if constexpr (kFold) {
+                // O^T joins the folded sums every kFoldTiles tiles; a moved
+                // reference rescales both (this warp: 64 of the 128 columns)
+                const bool fold = t > 0 && t % kFoldTiles == 0;
+                if (moved || fold) {
+                    ok = pwait(sm, &sm.o_done, (u - 1) & 1u, p.flags, kWaitEmpty) && ok;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t ta = lane_base + kColO + 64 * hh + 32 * c, tf = ta + RR;
+                        const float *al = &sm.alpha[64 * hh + 32 * c];
+                        uint32_t v[32], f[32];
+                        tmem_ld32(ta, v);
+                        if (t > kFoldTiles)  // (folded sums exist from the first fold on)
+                            tmem_ld32(tf, f);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float k = moved ? al[e] : 1.f;
+                            float x = __uint_as_float(v[e]) * k;
+                            float y = t > kFoldTiles ? __uint_as_float(f[e]) * k : 0.f;
+                            y += fold ? x : 0.f;
+                            v[e] = __float_as_uint(x);
+                            f[e] = __float_as_uint(y);
+                        }
+                        if (!fold)
+                            tmem_st32(ta, v);
+                        if (fold || t > kFoldTiles)
+                            tmem_st32(tf, f);
                     }
                     tmem_wait_st();
                 }
@@ -424,6 +473,11 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             tmem_ld32(lane_base + kColO + r0, hi);
             tmem_ld32(lane_base + kColO + RR + r0, lo);
             tmem_wait_ld();
+            if (kFold && n <= kFoldTiles) {  // nothing was folded
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    lo[e] = 0u;
+            }
             if (write) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -450,7 +504,10 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
     }
 }
 
-template <bool kG, bool kWin, class P>
+// kWin: sliding windows.  kFold: long ones, whose O^T is folded into a second
+// accumulator (ring.cuh); both fit tensor memory only with P's two parts in the
+// same columns, sixteen products of N = 128 a tile instead of eight of 256.
+template <bool kG, bool kWin, bool kFold, class P>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ PrArgs<kG, P> a)
 {
@@ -499,10 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0)
-            pr_issuer(a, sm);
+            pr_issuer<kFold>(a, sm);
         __syncwarp();
     } else {
-        pr_softmax<kWin>(a, sm, warp, lane);
+        pr_softmax<kWin, kFold>(a, sm, warp, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -526,7 +583,7 @@ bool prompt_supported(const AttnParams &p)
     return p.D == DD && pool_rows_fit(p);
 }
 
-template <bool kG, bool kWin, class P>
+template <bool kG, bool kWin, bool kFold, class P>
 cudaError_t launch_prompt(const P &p, int grid, cudaStream_t stream)
 {
     PrArgs<kG, P> a;
@@ -540,10 +597,10 @@ cudaError_t launch_prompt(const P &p, int grid, cudaStream_t stream)
             return cudaErrorInvalidValue;
     }
     static std::atomic<bool> configured[kMaxDevices];
-    const cudaError_t e = set_smem_limit_once(attn_prompt_kernel<kG, kWin, P>, kPrSmemBytes, configured);
+    const cudaError_t e = set_smem_limit_once(attn_prompt_kernel<kG, kWin, kFold, P>, kPrSmemBytes, configured);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(attn_prompt_kernel<kG, kWin, P>, dim3(grid), dim3(kThreads), kPrSmemBytes,
+    return launch_dependent(attn_prompt_kernel<kG, kWin, kFold, P>, dim3(grid), dim3(kThreads), kPrSmemBytes,
                             stream, a);
 }
 
@@ -551,14 +608,20 @@ cudaError_t launch_prompt(const P &p, int grid, cudaStream_t stream)
 // other page sizes assemble each tile from page pieces.
 cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t stream)
 {
-    return p.P % PT != 0 ? launch_prompt<true, false>(p, grid, stream)
-                         : launch_prompt<false, false>(p, grid, stream);
+    return p.P % PT != 0 ? launch_prompt<true, false, false>(p, grid, stream)
+                         : launch_prompt<false, false, false>(p, grid, stream);
 }
 
-// Sliding windows start and end inside tiles: pieces at any page size.
+// Sliding windows start and end inside tiles: pieces at any page size.  Windows
+// of more than kFoldWindow positions fold: 2 streams x 4,096 rows x 32 heads
+// over 4,096 positions take 1,303 us without and 1,548 with, off by 5e-6 and
+// 3e-6 of the output's norm; over 8,192 it would be 8e-6 without, and growing.
+constexpr int kFoldWindow = 4608;
+
 cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream)
 {
-    return launch_prompt<true, true>(p, grid, stream);
+    return (int64_t)p.window + p.sinks > kFoldWindow ? launch_prompt<true, true, true>(p, grid, stream)
+                                                     : launch_prompt<true, true, false>(p, grid, stream);
 }
 
 }  // namespace tfp

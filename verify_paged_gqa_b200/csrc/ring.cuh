@@ -319,6 +319,17 @@ __device__ __forceinline__ void ring_producer_pieces(const P &p, const CUtensorM
     __syncwarp();
 }
 
+// The tensor cores truncate their sums, so an O^T that grows over a long window
+// loses a little towards zero at every product (64 tiles: 7e-6 of the output's
+// norm).  The sliding-window kernels therefore add O^T to a second accumulator
+// in fp32, with rounding, every kFoldTiles tiles and start it anew: 2e-6 at any
+// length, which is what P's two bf16 parts leave.
+constexpr int kFoldTiles = 8;
+
+// Whether the PV product of a segment's tile t adds to O^T (else it starts it).
+__device__ __forceinline__ bool pv_adds(const AttnParams &, int t) { return t > 0; }
+__device__ __forceinline__ bool pv_adds(const WinParams &, int t) { return t % kFoldTiles != 0; }
+
 // Two probabilities as bf16 pairs hi and lo with p = hi + lo: both truncated
 // (|p - hi - lo| < 2^-14 p), or under kRn both rounded to nearest (at most
 // 2^-18 p, without a bias), at the same number of instructions.

@@ -1,4 +1,5 @@
 """Sliding-window attention with sinks against its definition in 64 bits (B200)."""
+import functools
 import math
 
 import pytest
@@ -7,6 +8,14 @@ import torch
 import window_ref
 
 pytestmark = pytest.mark.gpu
+
+
+TENSOR_CORE, CLUSTER = 1, 2
+
+
+@functools.cache
+def big_workspace():
+    return torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
 
 
 class WindowCase:
@@ -54,7 +63,7 @@ class WindowCase:
             self.v_pool[page, :, :hi - lo] = self.v[s][lo:hi].transpose(0, 1)
         self.table = self.table.cuda()
 
-    def call(self, window=None, sinks=None, max_len=None, out=None, ws=None):
+    def call(self, window=None, sinks=None, max_len=None, out=None, ws=None, kernel=None):
         import verify_paged_gqa_b200 as tf
         window = self.window if window is None else window
         sinks = self.sinks if sinks is None else sinks
@@ -63,6 +72,9 @@ class WindowCase:
               tf.tf_paged_attn_verify_window if self.rows <= 8 else tf.tf_paged_attn_prompt_window)
         if ws is None:
             ws = self.workspace(max_len)
+        if kernel is not None:   # one of the two, whichever the library would take
+            fn = lambda *a: tf.tf_testing_paged_attn_window(*a, kernel=kernel)  # noqa: E731
+            ws = big_workspace()
         if out is None:
             out = torch.full(self.q.shape, float("nan"), dtype=torch.float32, device="cuda")
         fn(self.k_pool, self.v_pool, self.table, self.lens, self.q, window, sinks, self.scale, out, ws, max_len)
@@ -92,6 +104,8 @@ def test_short_windows(d, G, P, rows, window, sinks):
     lens = [rows, rows + window + sinks, 700 + rows, 1024, max(rows, window + sinks + 1), 1537]
     c = WindowCase(lens, rows, window, sinks, d=d, G=G, P=P, seed=d + G + P + rows + window + sinks, edge=0.5)
     c.check(c.call())
+    c.check(c.call(kernel=TENSOR_CORE))
+    c.check(c.call(kernel=CLUSTER))
 
 
 @pytest.mark.parametrize("P", [512, 128, 100, 37, 5, 1])
@@ -101,12 +115,15 @@ def test_prompt_chunks(P, rows, G, window, sinks):
     lens = [rows, rows + 1000, max(rows, window + sinks), 641]
     c = WindowCase(lens, rows, window, sinks, G=G, P=P, seed=P + rows + window, edge=0.5)
     c.check(c.call())
+    c.check(c.call(kernel=TENSOR_CORE))
+    c.check(c.call(kernel=CLUSTER))
 
 
 @pytest.mark.parametrize("d,rows", [(256, 64), (512, 33)])
 def test_prompt_chunks_of_wide_heads(d, rows):
     c = WindowCase([rows, 900], rows, 200, 4, d=d, G=8, P=64, seed=d, edge=0.5)
-    c.check(c.call())
+    c.check(c.call(kernel=TENSOR_CORE))
+    c.check(c.call(kernel=CLUSTER))
 
 
 @pytest.mark.parametrize("rows,G,window,sinks,lens", [
@@ -115,15 +132,17 @@ def test_prompt_chunks_of_wide_heads(d, rows):
     (8, 8, 2048, 4, [20000, 2055, 131072]), (512, 4, 1024, 4, [9216, 600]), (1, 4, 30000, 1000, [40000, 31001])])
 def test_long_contexts_over_many_cta_ranges(rows, G, window, sinks, lens):
     c = WindowCase(lens, rows, window, sinks, G=G, P=512, Hkv=2, seed=rows + window)
-    c.check(c.call())
+    c.check(c.call(kernel=TENSOR_CORE))
+    c.check(c.call(kernel=CLUSTER))
 
 
 def test_many_streams_and_repeated_runs_are_bitwise_equal():
     lens = [1 + (37 * i) % 900 for i in range(150)]
     c = WindowCase(lens, 1, 200, 4, P=64, Hkv=1, seed=5)
-    a = c.call()
-    c.check(a)
-    assert torch.equal(a, c.call())
+    for kernel in (TENSOR_CORE, CLUSTER):
+        a = c.call(kernel=kernel)
+        c.check(a)
+        assert torch.equal(a, c.call(kernel=kernel))
 
 
 @pytest.mark.parametrize("d", [128, 256, 512])
@@ -131,10 +150,11 @@ def test_many_streams_and_repeated_runs_are_bitwise_equal():
 def test_a_window_past_every_length_sees_the_whole_context(d, rows):
     """The same set of positions, however it is said: equal outputs, bit for bit."""
     c = WindowCase([rows, 300 + rows, 1111], rows, 1 << 20, 0, d=d, seed=d + rows)
-    a = c.call()
-    c.check(a)
-    assert torch.equal(a, c.call(window=2 ** 31 - 1, sinks=2 ** 31 - 1))
-    assert torch.equal(a, c.call(window=1, sinks=c.max_len))
+    for kernel in (TENSOR_CORE, CLUSTER):
+        a = c.call(kernel=kernel)
+        c.check(a)
+        assert torch.equal(a, c.call(window=2 ** 31 - 1, sinks=2 ** 31 - 1, kernel=kernel))
+        assert torch.equal(a, c.call(window=1, sinks=c.max_len, kernel=kernel))
 
 
 @pytest.mark.parametrize("d,G,rows,window,lens", [
@@ -152,7 +172,23 @@ def test_growing_scores(d, G, rows, window, lens):
             if page >= 0:
                 rows_k = c.k[s][j * 512:(j + 1) * 512]
                 c.k_pool[page, :, :rows_k.shape[0]] = rows_k.transpose(0, 1)
-    c.check(c.call())
+    c.check(c.call(kernel=TENSOR_CORE))
+    c.check(c.call(kernel=CLUSTER))
+
+
+@pytest.mark.parametrize("d,G,P,rows", [(128, 8, 512, 8), (512, 8, 64, 4), (128, 4, 37, 200)])
+def test_a_withheld_arrival_times_out_and_the_next_call_is_clean(d, G, P, rows):
+    """The tensor-core kernels' bounded waits, as in the plain calls' failure test."""
+    import verify_paged_gqa_b200 as tf
+    c = WindowCase([60000, 3000], rows, 20000, 4, d=d, G=G, P=P, Hkv=1, seed=d + rows)
+    ws, out = big_workspace(), torch.zeros(c.q.shape, dtype=torch.float32, device="cuda")
+    tf.tf_workspace_status(ws)
+    tf.tf_testing_paged_attn_window(c.k_pool, c.v_pool, c.table, c.lens, c.q, 20000, 4, c.scale, out, ws, c.max_len,
+                                    kernel=TENSOR_CORE, wait_limit_cycles=20_000_000, withhold=1)
+    torch.cuda.synchronize()
+    ws[4:8].zero_()
+    assert tf.tf_workspace_status(ws) & tf.TF_DEV_TIMEOUT
+    c.check(c.call(kernel=TENSOR_CORE))
 
 
 def test_lengths_out_of_range_and_bad_pages_are_reported():

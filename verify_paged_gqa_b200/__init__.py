@@ -16,7 +16,7 @@ _EXPORTS = (
     "tf_paged_attn_decode_window", "tf_paged_attn_verify_window", "tf_paged_attn_prompt_window",
     "tf_paged_attn_window_workspace_bytes", "Rope", "tf_kv_put_rows_rope", "tf_kv_pages_fork",
     "tf_kv_pages_free", "tf_kv_pages_free_window", "tf_kv_pages_grow", "tf_kv_pages_compact",
-    "tf_kv_pages_move", "TF_DEV_NO_PAGE", "TF_MOVE_BYTES",
+    "tf_kv_pages_move", "tf_testing_paged_attn_window", "TF_DEV_NO_PAGE", "TF_MOVE_BYTES",
 )
 __all__ = list(_EXPORTS)
 

@@ -135,6 +135,9 @@ for _name in ("fork", "free", "free_window", "grow", "compact", "move"):
 raw.tf_testing_paged_attn.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _i32, _i32, _f32,
                                       _vp, _vp, _sz, ctypes.c_int64, _i32, _vp]
 raw.tf_testing_paged_attn.restype = ctypes.c_int
+raw.tf_testing_paged_attn_window.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _i32, _i32, _i32,
+                                             _i32, _f32, _vp, _vp, _sz, _i32, _i64, _i32, _vp]
+raw.tf_testing_paged_attn_window.restype = ctypes.c_int
 raw.tf_workspace_status.argtypes = [_vp, _P(ctypes.c_uint32), _vp]
 raw.tf_workspace_status.restype = ctypes.c_int
 raw.tf_status_str.argtypes = [ctypes.c_int]
@@ -235,7 +238,7 @@ def tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, position
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     rc = _binding.tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, positions,
-                                      rope.address, max_len, q_out, stream)
+                                      rope.inv_freq, rope.address, max_len, q_out, stream)
     if rc:
         raise TFError(rc, "tf_kv_put_rows_rope")
     return q_out
@@ -437,6 +440,26 @@ def tf_testing_paged_attn(k_pool, v_pool, table, lens, q, scale, out, workspace,
                                      workspace.data_ptr(), ws_bytes, int(wait_limit_cycles),
                                      int(withhold), _stream(stream)),
            "tf_testing_paged_attn")
+    return out
+
+
+def tf_testing_paged_attn_window(k_pool, v_pool, table, lens, q, window, sinks, scale, out,
+                                 workspace, max_len, kernel=0, wait_limit_cycles=4000000000,
+                                 withhold=0, stream=None):
+    """The sliding-window test hook of include/tf_paged_testing.h: kernel 0 is
+    the library's choice, 1 the tensor-core kernels, 2 the cluster kernel."""
+    _need(q, torch.bfloat16, 4, "q")
+    _need(out, torch.float32, 4, "out")
+    if tuple(out.shape) != tuple(q.shape):
+        raise ValueError("out must have q's shape")
+    pool, st = _pool(k_pool, v_pool), _streams(table, lens, max_len)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    _check(raw.tf_testing_paged_attn_window(ctypes.byref(pool), ctypes.byref(st), q.data_ptr(),
+                                            q.shape[2], q.shape[1], int(window), int(sinks),
+                                            float(scale), out.data_ptr(), workspace.data_ptr(),
+                                            ws_bytes, int(kernel), int(wait_limit_cycles),
+                                            int(withhold), _stream(stream)),
+           "tf_testing_paged_attn_window")
     return out
 
 

@@ -299,20 +299,20 @@ PyObject *attn_window(PyObject *, PyObject *const *args, Py_ssize_t n)
     });
 }
 
-// (k_pool, v_pool, table, lens, q or None, k_rows, v_rows, positions, address
-// of the tf_rope, max_len, q_out or None, stream)
+// (k_pool, v_pool, table, lens, q or None, k_rows, v_rows, positions, the
+// rope's inv_freq, address of the tf_rope, max_len, q_out or None, stream)
 PyObject *put_rows_rope(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
-    return guarded<12>(args, n, [](PyObject *const *a) {
+    return guarded<13>(args, n, [](PyObject *const *a) {
         Devices dev;
-        const auto *rope = (const tf_rope *)PyLong_AsVoidPtr(a[8]);
+        const auto *rope = (const tf_rope *)PyLong_AsVoidPtr(a[9]);
         if (!rope)
             throw PyError{};
         const at::Tensor &pos = need(a[7], at::kInt, 3, "positions");
         const at::Tensor &k = need_strided(a[5], at::kBFloat16, 4, "k_rows"),
                          &v = need_strided(a[6], at::kBFloat16, 4, "v_rows");
         const tf_kv_pool pool = pool_of(a[0], a[1], dev);
-        const tf_streams st = streams_of(a[2], a[3], a[9], dev);
+        const tf_streams st = streams_of(a[2], a[3], a[10], dev);
         must(pos.size(0) == st.n_streams && pos.size(2) == rope->n_axes,
              "positions must be [n_streams][rows][n_axes]");
         const int64_t W = pos.size(1);
@@ -325,7 +325,7 @@ PyObject *put_rows_rope(PyObject *, PyObject *const *args, Py_ssize_t n)
             must(t.size(2) <= INT32_MAX, "q is too large");
             heads = (int32_t)t.size(2);
             q = rows_of(t, st.n_streams, W, heads, pool.head_dim, "q", dev);
-            const at::Tensor &o = need(a[10], at::kBFloat16, 4, "q_out");
+            const at::Tensor &o = need(a[11], at::kBFloat16, 4, "q_out");
             must(o.sizes() == t.sizes(), "q_out must have q's shape");
             dev.on(o, "q_out");
             q_out = o.data_ptr();
@@ -333,7 +333,10 @@ PyObject *put_rows_rope(PyObject *, PyObject *const *args, Py_ssize_t n)
         const Rows kr = rows_of(k, st.n_streams, W, pool.n_kv_heads, pool.head_dim, "k_rows", dev);
         const Rows vr = rows_of(v, st.n_streams, W, pool.n_kv_heads, pool.head_dim, "v_rows", dev);
         dev.on(pos, "positions");
-        void *stream = stream_of(dev, a[11]);
+        const at::Tensor &freq = need(a[8], at::kFloat, 1, "inv_freq");
+        must(freq.data_ptr() == rope->inv_freq, "the rope's inv_freq has moved");
+        dev.on(freq, "inv_freq");
+        void *stream = stream_of(dev, a[12]);
         return lib.tf_kv_put_rows_rope(&pool, &st, rope, (const int32_t *)pos.data_ptr(), q.data, q.stride, q_out,
                                        heads, kr.data, kr.stride, vr.data, vr.stride, (int32_t)W, stream);
     });

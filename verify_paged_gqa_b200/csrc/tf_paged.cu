@@ -88,10 +88,12 @@ constexpr int kEntrySimt = 0;
 // max_len on (measured crossover near 5,700 positions).
 constexpr int kPmDecodeMinLen = 6144;
 
-// A sliding-window call's host arguments (window 0: a plain call).
+// A sliding-window call's host arguments.  `kernel` (tests only): 0 the
+// library's choice, 1 the tensor-core kernels, 2 the cluster kernel.
 struct Window {
     int32_t window = 0;
     int32_t sinks = 0;
+    int32_t kernel = 0;
 };
 
 struct Plan {
@@ -118,7 +120,7 @@ bool pool_rows_past_31_bits(const tf_kv_pool *pool)
 //   tensor core  18 to 28 us to start and merge, then 1.6, 2.6 or 4.6 us per
 //                128-position tile, and 6 to 14 per unit
 // Sets p.RB and p.whole for the cluster kernel when it is taken.
-bool takes_win_kernel(WinParams &p, int sms)
+bool takes_win_kernel(WinParams &p, int sms, int forced)
 {
     const int d = p.D == 128 ? 0 : p.D == 256 ? 1 : 2;
     WinParams c = p;
@@ -135,7 +137,7 @@ bool takes_win_kernel(WinParams &p, int sms)
     const int64_t tiles2 = 2 * ((seen + 127) / 128) + 1;  // (half a tile more for the edges)
     constexpr int kStart[3] = {180, 210, 280}, kTile[3] = {16, 26, 46}, kUnit[3] = {60, 100, 140};
     const int64_t tensor = kStart[d] + heads * blocks * (tiles2 * kTile[d] / 2 + kUnit[d]) / sms;
-    if (cluster >= tensor)
+    if (forced == 1 || (forced == 0 && cluster >= tensor))
         return false;
     p.RB = c.RB;
     p.whole = split.C;
@@ -220,7 +222,7 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         rc = device_sm_count(&sms);
         if (rc != TF_OK)
             return rc;
-        if (takes_win_kernel(p, sms)) {
+        if (takes_win_kernel(p, sms, win->kernel)) {
             plan->kernel = Kernel::kWin;
         } else if (nr > 0) {
             plan->kernel = Kernel::kPm;
@@ -472,6 +474,8 @@ int tf_kv_put_rows_rope(const tf_kv_pool *pool, const tf_streams *streams, const
             return TF_EINVAL;
         p.pair_axis[i] = rope->pair_axis[i];
     }
+    if (((int64_t)n_q_heads + 2 * (int64_t)pool->n_kv_heads) * pool->head_dim > INT32_MAX)
+        return TF_EINVAL;
     const int64_t q_row = (int64_t)n_q_heads * pool->head_dim;
     const int64_t kv_row = (int64_t)pool->n_kv_heads * pool->head_dim;
     if ((n_q_heads > 0 && (q_stride < q_row || q_stride % 8 != 0)) || k_stride < kv_row ||
@@ -738,7 +742,7 @@ size_t tf_paged_attn_window_workspace_bytes(const tf_kv_pool *pool, const tf_str
                                             int32_t n_q_heads, int32_t rows, int32_t window,
                                             int32_t sinks)
 {
-    const Window win{window, sinks};
+    const Window win{window, sinks, 0};
     Plan plan;
     if (make_plan(pool, streams, n_q_heads, rows, 4096, false, &plan, &win) != TF_OK)
         return 0;
@@ -749,7 +753,7 @@ int tf_paged_attn_decode_window(const tf_kv_pool *pool, const tf_streams *stream
                                 int32_t n_q_heads, int32_t window, int32_t sinks, float scale,
                                 float *out, void *workspace, size_t workspace_bytes, void *stream)
 {
-    const Window win{window, sinks};
+    const Window win{window, sinks, 0};
     return attn_call(pool, streams, q, n_q_heads, 1, 1, nullptr, scale, out, workspace,
                      workspace_bytes, stream, Faults{}, &win);
 }
@@ -759,7 +763,7 @@ int tf_paged_attn_verify_window(const tf_kv_pool *pool, const tf_streams *stream
                                 float scale, float *out, void *workspace, size_t workspace_bytes,
                                 void *stream)
 {
-    const Window win{window, sinks};
+    const Window win{window, sinks, 0};
     return attn_call(pool, streams, q, n_q_heads, rows, 8, nullptr, scale, out, workspace,
                      workspace_bytes, stream, Faults{}, &win);
 }
@@ -769,7 +773,7 @@ int tf_paged_attn_prompt_window(const tf_kv_pool *pool, const tf_streams *stream
                                 float scale, float *out, void *workspace, size_t workspace_bytes,
                                 void *stream)
 {
-    const Window win{window, sinks};
+    const Window win{window, sinks, 0};
     return attn_call(pool, streams, q, n_q_heads, rows, 4096, nullptr, scale, out, workspace,
                      workspace_bytes, stream, Faults{}, &win);
 }
@@ -788,6 +792,24 @@ int tf_testing_paged_attn(const tf_kv_pool *pool, const tf_streams *streams, con
     f.withhold = withhold;
     return attn_call(pool, streams, q, n_q_heads, rows, 4096, nullptr, scale, out, workspace,
                      workspace_bytes, stream, f);
+}
+
+int tf_testing_paged_attn_window(const tf_kv_pool *pool, const tf_streams *streams, const void *q,
+                                 int32_t n_q_heads, int32_t rows, int32_t window, int32_t sinks,
+                                 float scale, float *out, void *workspace, size_t workspace_bytes,
+                                 int32_t kernel, int64_t wait_limit_cycles, int32_t withhold,
+                                 void *stream)
+{
+    if (wait_limit_cycles < 1000000 || wait_limit_cycles > kWaitLimitCycles)
+        return TF_EINVAL;
+    if ((withhold != 0 && withhold != 1) || kernel < 0 || kernel > 2)
+        return TF_EINVAL;
+    Faults f;
+    f.wait_limit = wait_limit_cycles;
+    f.withhold = withhold;
+    const Window win{window, sinks, kernel};
+    return attn_call(pool, streams, q, n_q_heads, rows, 4096, nullptr, scale, out, workspace,
+                     workspace_bytes, stream, f, &win);
 }
 
 int tf_workspace_status(void *workspace, uint32_t *flags, void *stream)

@@ -23,7 +23,7 @@
 // order.
 //
 // The bookkeeping is a few kilobytes: a call's time is its latency, so each is
-// one kernel (compact a second, over the tables).  grow and compact scan
+// one kernel (compact over a table of more than 4,096 entries has a second).  grow and compact scan
 // refs with one block of 1,024 threads, 4 counts a thread.  pages_move is bound
 // by memory: 16 KB runs through a ring of four shared-memory stages with bulk
 // copies (TMA engine) in both directions, three blocks to an SM.
@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 constexpr int kScanPer = 4;                        // counts a thread takes at a time
+constexpr int64_t kRetableHere = 4096;             // table entries that compact's own block rewrites
 constexpr uint32_t kMoveChunk = 16384;             // bytes of one run
 constexpr int kMoveStages = 4;
 constexpr int kMoveBlocksPerSm = 3;
@@ -261,6 +262,27 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_grow_kernel(const __gri
     }
 }
 
+// Table entry i follows its page if that moved (the list's sources ascend:
+// binary search among `moves` of them; pages below n_live stay).
+__device__ __forceinline__ void retable(const PagesParams &p, int64_t i, int moves, int n_live)
+{
+    const int id = p.table[i];
+    if (id < n_live)
+        return;  // none, or a page that stays
+    int lo = 0, hi = moves;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (p.moves[1 + mid].x < id)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    if (lo < moves && p.moves[1 + lo].x == id)
+        p.table[i] = p.moves[1 + lo].y;
+    else
+        note(p.status, kDevBadPage);  // nobody holds this page
+}
+
 // One block.
 __global__ void __launch_bounds__(kScanThreads, 1) pages_compact_kernel(const __grid_constant__ PagesParams p)
 {
@@ -310,32 +332,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_compact_kernel(const __
     }
     if (threadIdx.x == 0)
         p.moves[0] = make_int4(movers, n_live, 0, 0);
+    const int64_t entries = (int64_t)p.S * p.stride;
+    if (entries <= kRetableHere)
+        for (int64_t i = threadIdx.x; i < entries; i += kScanThreads)
+            retable(p, i, movers, n_live);
 }
 
-// The table entries that name a moved page follow it (the list's sources
-// ascend: binary search).
+// Larger tables, by as many blocks as they need.
 __global__ void __launch_bounds__(256) pages_retable_kernel(const __grid_constant__ PagesParams p)
 {
     wait_prior_grid();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)p.S * p.stride)
-        return;
-    const int id = p.table[i];
     const int4 head = p.moves[0];
-    if (id < head.y)
-        return;  // none, or a page that stays
-    int lo = 0, hi = head.x;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (p.moves[1 + mid].x < id)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    if (lo < head.x && p.moves[1 + lo].x == id)
-        p.table[i] = p.moves[1 + lo].y;
-    else
-        note(p.status, kDevBadPage);  // nobody holds this page
+    if (i < (int64_t)p.S * p.stride)
+        retable(p, i, head.x, head.y);
 }
 
 // ---- the moves ---------------------------------------------------------------
@@ -500,7 +510,7 @@ cudaError_t launch_pages_compact(const PagesParams &p, cudaStream_t stream)
     pages_compact_kernel<<<1, kScanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     const int64_t entries = (int64_t)p.S * p.stride;
-    if (e != cudaSuccess || entries == 0)
+    if (e != cudaSuccess || entries <= kRetableHere)
         return e;
     return launch_dependent(pages_retable_kernel, dim3((unsigned)((entries + 255) / 256)), dim3(256), 0,
                             stream, p);

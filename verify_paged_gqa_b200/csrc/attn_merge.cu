@@ -65,12 +65,13 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         }
         return;
     }
-    if (p.whole == 1)
+    constexpr bool kPieces = std::is_same_v<P, WinParams>;
+    if (kPieces ? p.whole == 1 : p.whole != 0)
         return;  // every unit was finished whole by one CTA
     // the unit's tiles [U0, U1) and the CTAs that met them: warp 0 works them
     // out once for the block (lanes split the row blocks)
     __shared__ int nseg_sh;
-    if (p.whole) {
+    if (kPieces && p.whole) {
         // piece k of the unit left its partial in its CTA's first slot
         const int n = unit_tiles(p, len, b);
         const int c0 = (u * p.n_rblk + b) * p.whole;

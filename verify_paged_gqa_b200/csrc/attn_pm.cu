@@ -723,7 +723,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 mx = max_tree(x);
                 slow = block_any<NT>(mx > kRescaleLog2);
             }
-            bool moved = false;
+            [[maybe_unused]] bool moved_any = false;  // (sliding windows: used below)
             if (slow) {
                 // --- a new reference max for rows whose max grew past it ---
                 float y[32];
@@ -734,6 +734,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 xpose_reduce<32, true>(y, lane);
                 sm.red[wq][R0 + lane] = y[0];
                 named_barrier(1, NT);
+                bool moved = false;
                 if (st < NR) {
                     const float tmax = fmaxf(fmaxf(sm.red[0][st], sm.red[1][st]),
                                              fmaxf(sm.red[2][st], sm.red[3][st]));
@@ -747,7 +748,9 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                     moved = t > 0 && grow && m_old != NEG_INF;
                 }
                 moved = block_any<NT>(moved);  // also publishes mref / negm / alpha
-                if (kMask != kWindow && moved) {
+                if constexpr (kMask == kWindow) {
+                    moved_any = moved;
+                } else if (moved) {
                     // PV(u - 1) must be done before O^T is touched; this warp
                     // rescales its rows' hi and lo columns of every dim block
                     ok = pwait(sm, &sm.o_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u, p.flags,
@@ -791,6 +794,7 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 // O^T joins the folded sums every kFoldTiles tiles; a moved
                 // reference rescales both
                 const bool fold = t > 0 && t % kFoldTiles == 0;
+                const bool moved = moved_any;
                 if (moved || fold) {
                     ok = pwait(sm, &sm.o_done[(u - 1) & 1u], ((u - 1) >> 1) & 1u, p.flags,
                                kWaitEmpty) && ok;
@@ -877,7 +881,16 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
                 const float p1 = fast_exp2(x[2 * e + 1]);
                 l[2 * e] += p0;
                 l[2 * e + 1] += p1;
-                split_p<kMask == kWindow>(p0, p1, hw[e], lw[e]);
+                if constexpr (kMask == kWindow) {
+                    split_p(p0, p1, hw[e], lw[e]);
+                    continue;
+                }
+                // P = hi + lo, both bf16 by truncation: |p - hi - lo| < 2^-14 p
+                const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                hw[e] = __byte_perm(b0, b1, 0x7632);
+                const float r0 = p0 - __uint_as_float(b0 & 0xffff0000u);
+                const float r1 = p1 - __uint_as_float(b1 & 0xffff0000u);
+                lw[e] = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
             }
             // buffer u % kPBufs is free once PV(u - kPBufs) completed
             if (u >= (uint32_t)C::kPBufs) {

@@ -328,7 +328,7 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             const float hm = hmax == NEG_INF ? NEG_INF : hmax * sl;
             // a half that would move the row's reference calls for the slow path
             const bool hgrow = hm != NEG_INF && (mref == NEG_INF || hm > mref + kRescaleLog2);
-            bool moved = false;
+            [[maybe_unused]] bool moved = false;  // (long sliding windows: used below)
             if (block_any<256>(hgrow)) {
                 // the row's tile max from its two halves; both threads of the
                 // row take the same decision from the same values
@@ -347,8 +347,10 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                     sm.alpha[r] = al;
                 // rows with an earlier reference moved: rescale their O^T
                 // columns (this warp: the hi columns for hh = 0, lo for hh = 1)
-                moved = block_any<256>(grow && al != 0.f);
-                if (!kFold && moved) {
+                const bool any = block_any<256>(grow && al != 0.f);
+                if constexpr (kFold) {
+                    moved = any;
+                } else if (any) {
                     ok = pwait(sm, &sm.o_done, (u - 1) & 1u, p.flags, kWaitEmpty) && ok;
                     tc_fence_after();
 #pragma unroll 1
@@ -400,12 +402,14 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             }
             // V rows past the stream's end are zeroed (0 * NaN = NaN): the two
             // threads of position r take one 64-dim box each
-            const TileRows rows = tile_rows(p, it, tpos, min(it.len - tpos, PT));
-            if (tpos + PT > it.len || rows.a < rows.b) {
+            TileRows rows = {PT, PT};
+            if constexpr (kWin)
+                rows = tile_rows(p, it, tpos, min(it.len - tpos, PT));
+            if (tpos + PT > it.len || (kWin && rows.a < rows.b)) {
                 const uint32_t uv = ring_v_unit(1, u0, t, n);
                 const int st = (int)(uv % NU);
                 ok = pwait(sm, &sm.full[st], (uv / NU) & 1u, p.flags, kWaitFull) && ok;
-                if (r >= it.len - tpos || (r >= rows.a && r < rows.b)) {
+                if (r >= it.len - tpos || (kWin && r >= rows.a && r < rows.b)) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         *reinterpret_cast<uint4 *>(sm.ring[st] + hh * kRingBox + sw128_off(r, c)) =
@@ -426,7 +430,7 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                     const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                     lacc = __fadd2_rn(lacc, pp);
                     if constexpr (kWin) {
-                        split_p<true>(pp.x, pp.y, hw[e], lw[e]);
+                        split_p(pp.x, pp.y, hw[e], lw[e]);
                         continue;
                     }
                     // P = hi + lo, both bf16 by truncation: |p - hi - lo| < 2^-14 p

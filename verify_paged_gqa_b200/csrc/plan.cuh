@@ -42,6 +42,8 @@
 
 #include "common.cuh"
 
+#include <type_traits>
+
 namespace tfp {
 
 constexpr int kTile = 128;     // positions per scheduling tile
@@ -147,7 +149,8 @@ __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
         // CTA c takes piece c mod whole of unit c / whole (stream, KV head, row
         // block): the unit's tiles in `whole` runs of nearly equal length
         const int per_s = p.Hkv * p.n_rblk;
-        const int c = blockIdx.x / p.whole;
+        constexpr bool kPieces = std::is_same_v<P, WinParams>;  // (plain calls: whole units)
+        const int c = kPieces ? blockIdx.x / p.whole : blockIdx.x;
         const int s = c / per_s;
         const int len = s < p.S ? __ldg(p.lens + s) : 0;
         const long long hw = s < p.S ? head_work(p, len) : 0;
@@ -162,13 +165,19 @@ __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
                 long long before = 0;
                 for (int bb = 0; bb < b; ++bb)
                     before += unit_work(p, len, bb);
-                const int j = blockIdx.x % p.whole;
-                const int n = unit_tiles(p, len, b);
-                const int t0 = piece_start(n, j, p.whole), t1 = piece_start(n, j + 1, p.whole);
-                if (t1 > t0) {
+                if constexpr (!kPieces) {
                     out.s0 = s;
-                    out.off0 = kh * hw + before + p.VT + t0;
-                    out.g1 = t1 - t0;
+                    out.off0 = kh * hw + before;
+                    out.g1 = unit_work(p, len, b);
+                } else {
+                    const int j = blockIdx.x - c * p.whole;
+                    const int n = unit_tiles(p, len, b);
+                    const int t0 = piece_start(n, j, p.whole), t1 = piece_start(n, j + 1, p.whole);
+                    if (t1 > t0) {
+                        out.s0 = s;
+                        out.off0 = kh * hw + before + p.VT + t0;
+                        out.g1 = t1 - t0;
+                    }
                 }
             }
         }

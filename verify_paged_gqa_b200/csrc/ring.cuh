@@ -330,23 +330,14 @@ constexpr int kFoldTiles = 8;
 __device__ __forceinline__ bool pv_adds(const AttnParams &, int t) { return t > 0; }
 __device__ __forceinline__ bool pv_adds(const WinParams &, int t) { return t % kFoldTiles != 0; }
 
-// Two probabilities as bf16 pairs hi and lo with p = hi + lo: both truncated
-// (|p - hi - lo| < 2^-14 p), or under kRn both rounded to nearest (at most
-// 2^-18 p, without a bias), at the same number of instructions.
-template <bool kRn>
+// Two probabilities as bf16 pairs hi and lo, both rounded to nearest: p = hi +
+// lo to 2^-18 p and without a bias, at the instructions that truncating both
+// takes (2^-14 p, always low).
 __device__ __forceinline__ void split_p(float p0, float p1, uint32_t &hi, uint32_t &lo)
 {
-    if constexpr (kRn) {
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
-        const float r0 = p0 - bf_lo(hi), r1 = p1 - bf_hi(hi);
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(r1), "f"(r0));
-    } else {
-        const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-        hi = __byte_perm(b0, b1, 0x7632);
-        const float r0 = p0 - __uint_as_float(b0 & 0xffff0000u);
-        const float r1 = p1 - __uint_as_float(b1 & 0xffff0000u);
-        lo = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
-    }
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
+    const float r0 = p0 - bf_lo(hi), r1 = p1 - bf_hi(hi);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(r1), "f"(r0));
 }
 
 // Ring index of the first V unit of tile t of a segment that starts at the

@@ -586,7 +586,30 @@ __device__ __forceinline__ void pm_softmax(const A &a, PmSmem<D, NR> &sm, int wa
             }
             sm.rowoff[jj & 1u][st] = off;
         }
-        {
+        if constexpr (kMask == kWindow) {
+            // (a short call runs this once: little code, since it comes from a
+            // cold instruction cache, and the rows' offsets above for both ends)
+            named_barrier(1, NT);
+            ok = pwait(sm, &sm.q_free, (jj & 1u) ^ 1u, p.flags, kWaitQEmpty) && ok;
+#pragma unroll 1
+            for (int c = 0; c < kPer; c += 4) {
+                uint4 qv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int f = st + NT * (c + i);
+                    const long long off = sm.rowoff[jj & 1u][f / (D / 8)];
+                    qv[i] = make_uint4(0, 0, 0, 0);
+                    if (off >= 0)
+                        qv[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + off) + f % (D / 8));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int f = st + NT * (c + i);
+                    const int r = f / (D / 8), k = f % (D / 8);
+                    *reinterpret_cast<uint4 *>(sm.q + (k >> 3) * (NR * 128) + sw128_off(r, k & 7)) = qv[i];
+                }
+            }
+        } else {
             uint4 qv[kPer];
 #pragma unroll
             for (int c = 0; c < kPer; ++c) {

@@ -132,10 +132,10 @@ __host__ __device__ __forceinline__ int piece_start(int n, int j, int pieces)
 
 // This CTA's range, found by warp 0 at kernel start.
 struct CtaRange {
-    long long g0, g1;   // work tiles [g0, g1) of the launch
-    long long off0;     // g0's offset inside stream s0
+    long long g0, g1;   // work tiles [g0, g1) of the launch (whole pieces: of the unit)
+    long long off0;     // g0's offset inside stream s0 (whole pieces: the row block)
     int s0;             // stream holding tile g0 (S when the range is empty)
-    int pad;
+    int kh0;            // whole pieces: the KV head
 };
 
 // Run by one whole warp.  Two passes over the streams' lengths, 32 at a
@@ -145,12 +145,29 @@ struct CtaRange {
 template <class P>
 __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
 {
-    if (p.whole) {
+    constexpr bool kPieces = std::is_same_v<P, WinParams>;
+    if (kPieces && p.whole) {
         // CTA c takes piece c mod whole of unit c / whole (stream, KV head, row
         // block): the unit's tiles in `whole` runs of nearly equal length
+        if (lane == 0) {
+            int u = blockIdx.x / p.whole;
+            const int j = blockIdx.x - u * p.whole;
+            const int b = u % p.n_rblk;
+            u /= p.n_rblk;
+            const int s = u / p.Hkv, len = __ldg(p.lens + s);
+            const int n = len_ok(p, len) ? unit_tiles(p, len, b) : 0;
+            out.g0 = piece_start(n, j, p.whole);
+            out.g1 = piece_start(n, j + 1, p.whole);
+            out.off0 = b;
+            out.s0 = out.g1 > out.g0 ? s : p.S;
+            out.kh0 = u % p.Hkv;
+        }
+        return;
+    }
+    if (p.whole) {
+        // CTA c takes unit c (stream, KV head, row block) whole
         const int per_s = p.Hkv * p.n_rblk;
-        constexpr bool kPieces = std::is_same_v<P, WinParams>;  // (plain calls: whole units)
-        const int c = kPieces ? blockIdx.x / p.whole : blockIdx.x;
+        const int c = blockIdx.x;
         const int s = c / per_s;
         const int len = s < p.S ? __ldg(p.lens + s) : 0;
         const long long hw = s < p.S ? head_work(p, len) : 0;
@@ -165,20 +182,9 @@ __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
                 long long before = 0;
                 for (int bb = 0; bb < b; ++bb)
                     before += unit_work(p, len, bb);
-                if constexpr (!kPieces) {
-                    out.s0 = s;
-                    out.off0 = kh * hw + before;
-                    out.g1 = unit_work(p, len, b);
-                } else {
-                    const int j = blockIdx.x - c * p.whole;
-                    const int n = unit_tiles(p, len, b);
-                    const int t0 = piece_start(n, j, p.whole), t1 = piece_start(n, j + 1, p.whole);
-                    if (t1 > t0) {
-                        out.s0 = s;
-                        out.off0 = kh * hw + before + p.VT + t0;
-                        out.g1 = t1 - t0;
-                    }
-                }
+                out.s0 = s;
+                out.off0 = kh * hw + before;
+                out.g1 = unit_work(p, len, b);
             }
         }
         return;
@@ -284,6 +290,12 @@ struct SegCursor {
             return;
         }
         len = __ldg(p.lens + s);
+        if (std::is_same_v<P, WinParams> && p.whole) {
+            kh = r.kh0;
+            b = static_cast<int>(r.off0);
+            off = p.VT + static_cast<int>(r.g0);
+            return;
+        }
         const long long hw = head_work(p, len);
         kh = static_cast<int>(r.off0 / hw);
         int rem = static_cast<int>(r.off0 - kh * hw);

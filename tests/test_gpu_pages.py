@@ -231,6 +231,20 @@ def test_bad_entries_are_reported_and_left():
     assert int(c.status) == tf.TF_DEV_BAD_PAGE and c.d_refs.tolist() == c.refs
 
 
+def test_no_child_takes_a_page_that_nobody_holds():
+    """Many children of one parent look at the same count at once."""
+    import verify_paged_gqa_b200 as tf
+    stride, N = 300, 512
+    refs = dev([j % 2 for j in range(stride)])      # every other page has no holder
+    table, lens = dev([list(range(stride))]), dev([stride * 16])
+    new, new_lens = torch.full((N, stride), -9, dtype=torch.int32, device="cuda"), torch.zeros(N, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tf.tf_kv_pages_fork(refs, 16, table, lens, dev([0] * N), new, new_lens, status=status)
+    assert refs.tolist() == [(N + 1) * (j % 2) for j in range(stride)]
+    assert bool((new == dev([j if j % 2 else -1 for j in range(stride)])).all())
+    assert int(status) == tf.TF_DEV_BAD_PAGE
+
+
 def test_streams_of_pages_need_no_pages():
     import verify_paged_gqa_b200 as tf
     c = Cache(8, 16, 0, 2, seed=7)

@@ -85,11 +85,16 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(const __grid_constant__
             note(p.status, kDevBadPage);
             id = -1;
         }
-        if (id >= 0 && atomicAdd(p.refs + id, 1) <= 0) {
-            // (a page that nobody holds: its next owner would share it)
-            atomicSub(p.refs + id, 1);
-            note(p.status, kDevBadPage);
-            id = -1;
+        if (id >= 0) {
+            // A page that nobody holds is not taken: its next owner would share
+            // it.  (Counts only rise here, and only from 1 on, so a 0 is one
+            // for every child that looks.)
+            if (__ldcg(p.refs + id) <= 0) {
+                note(p.status, kDevBadPage);
+                id = -1;
+            } else {
+                atomicAdd(p.refs + id, 1);
+            }
         }
     }
     p.dst_table[(int64_t)c * p.dst_stride + j] = id < 0 ? -1 : id;

@@ -201,7 +201,8 @@ TF_API int tf_kv_copy_state(const tf_kv_pool *src_pool, const tf_streams *src,
  * tables and lens alone (pages are taken lowest id first), so they may be
  * captured and replayed.  Calls on the same refs must be ordered by the
  * caller.
- *  refs  device int32 [n_pages], 16-byte aligned
+ *  refs  device int32 [n_pages], 16-byte aligned; n_pages and a table's stride
+ *        are at most 2^31 - 8193 (TF_EINVAL)
  * Every call takes an optional status word (device uint32, 4-byte aligned)
  * into which TF_DEV_* bits are ORed. */
 typedef struct tf_kv_pages {

@@ -141,3 +141,24 @@ def test_python_checks(lib):
         tf.tf_kv_pages_free(refs, 16, table, status=torch.zeros(1), stream=0)
     with pytest.raises(ValueError):
         tf.tf_kv_pages_fork(refs, 16, table, lens, i32(5), i32(4, 3), i32(4), stream=0)
+
+
+def test_page_counts_that_indexes_cannot_pass(lib):
+    """The kernels step past the last page and entry by up to a block's worth
+    in 32 bits: counts so near 2^31 are refused."""
+    raw, ok = lib.raw, lib.tf_kv_pages(PTR, 100, 16)
+    for n in (2 ** 31 - 1, 2 ** 31 - 8191):
+        many = lib.tf_kv_pages(PTR, n, 16)
+        assert raw.tf_kv_pages_free(ref(many), PTR, 4, 2, None, None, None, None) == lib.TF_EINVAL
+        assert raw.tf_kv_pages_grow(ref(many), PTR, 4, PTR, 2, 1, PTR, 1 << 20, None, None) == lib.TF_EINVAL
+        assert raw.tf_kv_pages_compact(ref(many), PTR, 4, 2, PTR, 1 << 40, None, None) == lib.TF_EINVAL
+        assert raw.tf_kv_pages_free(ref(ok), PTR, n, 1, None, None, None, None) == lib.TF_EINVAL
+        assert raw.tf_kv_pages_fork(ref(ok), PTR, 4, PTR, 2, PTR, 1, PTR, n, PTR, None, None) == lib.TF_EINVAL
+
+
+def test_a_stream_handle_that_is_no_pointer(lib):
+    import torch
+    import verify_paged_gqa_b200 as tf
+    none = torch.zeros((0, 3), dtype=torch.int32)
+    with pytest.raises(OverflowError):
+        tf.tf_kv_pages_free(torch.zeros(0, dtype=torch.int32), 16, none, stream=1 << 70)

@@ -139,8 +139,12 @@ void *stream_of(const Devices &dev, PyObject *o)
     dev.check();
     if (o == Py_None)
         return c10::cuda::getCurrentCUDAStream().stream();
-    if (PyLong_Check(o))
-        return PyLong_AsVoidPtr(o);
+    if (PyLong_Check(o)) {
+        void *s = PyLong_AsVoidPtr(o);
+        if (PyErr_Occurred())
+            throw PyError{};
+        return s;
+    }
     PyObject *handle = PyObject_GetAttrString(o, "cuda_stream");
     if (!handle)
         throw PyError{};
@@ -306,8 +310,9 @@ PyObject *put_rows_rope(PyObject *, PyObject *const *args, Py_ssize_t n)
     return guarded<13>(args, n, [](PyObject *const *a) {
         Devices dev;
         const auto *rope = (const tf_rope *)PyLong_AsVoidPtr(a[9]);
-        if (!rope)
+        if (PyErr_Occurred())
             throw PyError{};
+        must(rope != nullptr, "the rope has no address");
         const at::Tensor &pos = need(a[7], at::kInt, 3, "positions");
         const at::Tensor &k = need_strided(a[5], at::kBFloat16, 4, "k_rows"),
                          &v = need_strided(a[6], at::kBFloat16, 4, "v_rows");

@@ -386,14 +386,18 @@ int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Pages and entries of a table row at most: the kernels step past the last
+// one by up to a block's 4,096, in 32 bits.
+constexpr int32_t kMaxPages = INT32_MAX - 8192;
+
 // The checks every page call shares; fills the common parameters.
 int check_pages(const tf_kv_pages *pages, int32_t *table, int32_t stride, int32_t n_streams,
                 uint32_t *status, PagesParams *p)
 {
-    if (!pages || pages->n_pages < 1 || pages->page_size < 1 || !pages->refs ||
-        !aligned16(pages->refs) || !aligned4(status))
+    if (!pages || pages->n_pages < 1 || pages->n_pages > kMaxPages || pages->page_size < 1 ||
+        !pages->refs || !aligned16(pages->refs) || !aligned4(status))
         return TF_EINVAL;
-    if (n_streams < 0 || stride < 1 || (int64_t)n_streams * stride > INT32_MAX)
+    if (n_streams < 0 || stride < 1 || stride > kMaxPages || (int64_t)n_streams * stride > INT32_MAX)
         return TF_EINVAL;
     if (n_streams > 0 && (!table || !aligned4(table)))
         return TF_EINVAL;
@@ -576,7 +580,8 @@ int tf_kv_pages_fork(const tf_kv_pages *pages, const int32_t *src_table, int32_t
         check_pages(pages, const_cast<int32_t *>(src_table), src_stride, n_src, status, &p);
     if (rc != TF_OK)
         return rc;
-    if (n_dst < 0 || dst_stride < 1 || (int64_t)n_dst * dst_stride > INT32_MAX)
+    if (n_dst < 0 || dst_stride < 1 || dst_stride > kMaxPages ||
+        (int64_t)n_dst * dst_stride > INT32_MAX)
         return TF_EINVAL;
     if (n_src > 0 && !src_lens)
         return TF_EINVAL;

@@ -81,3 +81,84 @@ def test_a_window_layer_of_a_serving_loop(d, P, window, sinks, seed):
         assert int(status) == 0, int(status)
         assert tf.tf_workspace_status(ws) == 0
     assert step > 8
+
+
+def test_pages_past_offsets_of_32_bits():
+    """Pools of more than 2^32 values each (8.6 GB): rows are written, attended
+    to and moved at both ends."""
+    import verify_paged_gqa_b200 as tf
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    P, Hkv, G, d, n = 512, 8, 4, 128, 700
+    n_pages = 2 ** 32 // (P * Hkv * d) + 8
+    kp, vp = (torch.empty((n_pages, Hkv, P, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert kp.numel() > 2 ** 32
+    ids = [[n_pages - 1, 0], [1, n_pages - 2]]
+    refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    for page in sum(ids, []):
+        refs[page] = 1
+    table, lens = dev(ids), dev([n, n])
+    k, v = (torch.randn(2, n, Hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pos = torch.zeros(2, n, 1, dtype=torch.int32, device="cuda")     # the turn by 0 keeps every bit
+    tf.tf_kv_put_rows_rope(kp, vp, table, lens, None, k, v, pos, tf.Rope(torch.ones(d // 2, device="cuda")), n)
+    ws, moves = torch.zeros(32 << 20, dtype=torch.uint8, device="cuda"), torch.zeros((1 + n_pages // 2, 4), dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 8, Hkv * G, d, generator=g, device="cuda").to(torch.bfloat16)
+
+    def attend():
+        for kernel in (1, 2):
+            out = tf.tf_testing_paged_attn_window(kp, vp, table, lens, q, 300, 4, 0.1, torch.empty(q.shape, dtype=torch.float32, device="cuda"),
+                                                  ws, n, kernel=kernel)
+            for s in range(2):
+                ref, bound = window_ref.attend(q[s], k[s], v[s], 300, 4, 0.1)
+                assert ((out[s].double() - ref).abs() <= bound).all()
+    attend()
+    tf.tf_kv_pages_compact(refs, P, table, moves, status=status)
+    tf.tf_kv_pages_move(kp, vp, moves, status=status)
+    assert moves[0].tolist() == [2, 4, 0, 0] and table.tolist() == [[3, 0], [1, 2]]
+    attend()
+    # and out to the far end
+    moves[0, 0] = 1
+    moves[1] = dev([3, n_pages - 3, P, 0])
+    tf.tf_kv_pages_move(kp, vp, moves, status=status)
+    table[0, 0] = n_pages - 3
+    kp[3] = float("nan")
+    attend()
+    assert int(status) == 0 and tf.tf_workspace_status(ws) == 0
+
+
+FIRST_CALL = """
+import torch, verify_paged_gqa_b200 as tf
+i32 = dict(dtype=torch.int32, device="cuda")
+kp, vp = (torch.randn(8, 2, 64, 128, device="cuda").to(torch.bfloat16) for _ in range(2))
+table, lens, ws = torch.arange(8, **i32).view(2, 4), torch.full((2,), 200, **i32), torch.zeros(32 << 20, dtype=torch.uint8, device="cuda")
+refs, moves, status = torch.ones(8, **i32), torch.zeros((16, 4), **i32), torch.zeros(1, **i32)
+rope, pos = tf.Rope(torch.ones(64, device="cuda")), torch.ones((2, {rows}, 1), **i32)
+qkv = torch.randn(2, {rows}, 12, 128, device="cuda").to(torch.bfloat16)
+q_out = torch.zeros((2, {rows}, 8, 128), dtype=torch.bfloat16, device="cuda")
+out = torch.zeros((2, {rows}, 8, 128), device="cuda")
+def step():
+    tf.tf_kv_pages_grow(refs, 64, table, lens, {rows}, moves, status=status)
+    tf.tf_kv_pages_move(kp, vp, moves, status=status)
+    tf.tf_kv_put_rows_rope(kp, vp, table, lens, qkv[:, :, :8], qkv[:, :, 8:10], qkv[:, :, 10:], pos, rope, 256, q_out=q_out)
+    tf.tf_testing_paged_attn_window(kp, vp, table, lens, q_out, 100, 4, 0.1, out, ws, 256, kernel={kernel})
+    tf.tf_kv_pages_compact(refs, 64, table, moves, status=status)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+got = out.clone()
+out.zero_()
+step()
+assert bool(got.any()) and torch.equal(got, out)
+assert int(status) == 0 and tf.tf_workspace_status(ws) == 0
+"""
+
+
+@pytest.mark.parametrize("rows,kernel", [(1, 2), (8, 1), (100, 1)])
+def test_the_first_calls_of_a_process_may_be_captured(rows, kernel):
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.format(rows=rows, kernel=kernel)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

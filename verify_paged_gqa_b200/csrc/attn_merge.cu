@@ -41,6 +41,11 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
     const int u = blk / groups / p.n_rblk;
     const int kh = u % p.Hkv;
     const int s = u / p.Hkv;
+    constexpr bool kPieces = std::is_same_v<P, WinParams>;
+    // A window's calls follow the page calls, which write lengths: nothing is
+    // read here before they are complete, as in the partial kernels.
+    if (kPieces)
+        wait_prior_grid();
     const int len = __ldg(p.lens + s);
     const int mb = b * p.RB;                       // first row of the row block
     const int m0 = mb + g * kMergeRows;
@@ -50,7 +55,8 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
     const float NEG_INF = -__int_as_float(0x7f800000);
     // launched as a programmatic dependent of the partial kernel: wait for
     // that grid to complete (and its writes to be visible) before going on
-    wait_prior_grid();
+    if (!kPieces)
+        wait_prior_grid();
 
     if (!len_ok(p, len)) {
         if (threadIdx.x == 0 && kh == 0 && b == 0 && g == 0)
@@ -65,7 +71,6 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         }
         return;
     }
-    constexpr bool kPieces = std::is_same_v<P, WinParams>;
     if (kPieces ? p.whole == 1 : p.whole != 0)
         return;  // every unit was finished whole by one CTA
     // the unit's tiles [U0, U1) and the CTAs that met them: warp 0 works them

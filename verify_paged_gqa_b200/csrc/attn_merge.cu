@@ -35,17 +35,30 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
     const int lane = threadIdx.x % 32;
     const int nwarps = blockDim.x / 32;
     const int groups = (p.RB + kMergeRows - 1) / kMergeRows;
+    constexpr bool kPieces = std::is_same_v<P, WinParams>;
+    // A window's calls follow the page calls, which write lengths: nothing is
+    // read here before they are complete, as in the partial kernels.
+    if (kPieces)
+        wait_prior_grid();
+    if (kPieces && p.whole == 1) {
+        // Every unit was finished whole by one CTA; a block per stream is left
+        // to report lengths out of range.
+        if (!len_ok(p, __ldg(p.lens + blockIdx.x))) {
+            if (threadIdx.x == 0)
+                set_flag(p.flags, kDevBadLen);
+            const float nan = __int_as_float(0x7fc00000);
+            const size_t n = (size_t)p.W * p.Hq * (D / 4);
+            for (size_t e = threadIdx.x; e < n; e += blockDim.x)
+                reinterpret_cast<float4 *>(p.out)[blockIdx.x * n + e] = make_float4(nan, nan, nan, nan);
+        }
+        return;
+    }
     const int blk = blockIdx.x;
     const int g = blk % groups;
     const int b = (blk / groups) % p.n_rblk;
     const int u = blk / groups / p.n_rblk;
     const int kh = u % p.Hkv;
     const int s = u / p.Hkv;
-    constexpr bool kPieces = std::is_same_v<P, WinParams>;
-    // A window's calls follow the page calls, which write lengths: nothing is
-    // read here before they are complete, as in the partial kernels.
-    if (kPieces)
-        wait_prior_grid();
     const int len = __ldg(p.lens + s);
     const int mb = b * p.RB;                       // first row of the row block
     const int m0 = mb + g * kMergeRows;
@@ -71,7 +84,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__
         }
         return;
     }
-    if (kPieces ? p.whole == 1 : p.whole != 0)
+    if (!kPieces && p.whole)
         return;  // every unit was finished whole by one CTA
     // the unit's tiles [U0, U1) and the CTAs that met them: warp 0 works them
     // out once for the block (lanes split the row blocks)
@@ -230,7 +243,9 @@ template <int D, class P>
 cudaError_t launch_attn_merge(const P &p, cudaStream_t stream)
 {
     const int groups = (p.RB + kMergeRows - 1) / kMergeRows;
-    const int64_t blocks = (int64_t)p.S * p.Hkv * p.n_rblk * groups;
+    const int64_t blocks = std::is_same_v<P, WinParams> && p.whole == 1
+                               ? p.S
+                               : (int64_t)p.S * p.Hkv * p.n_rblk * groups;
     if (blocks == 0)
         return cudaSuccess;
     const int threads = 32 * min(kMergeRows, p.RB);

@@ -148,7 +148,9 @@ __device__ __forceinline__ void find_range(const P &p, CtaRange &out, int lane)
     constexpr bool kPieces = std::is_same_v<P, WinParams>;
     if (kPieces && p.whole) {
         // CTA c takes piece c mod whole of unit c / whole (stream, KV head, row
-        // block): the unit's tiles in `whole` runs of nearly equal length
+        // block): the unit's tiles in `whole` runs of nearly equal length.  (Of
+        // more units than CTAs it takes whole ones: unit c, c + grid, ..., the
+        // later ones by SegCursor.)
         if (lane == 0) {
             int u = blockIdx.x / p.whole;
             const int j = blockIdx.x - u * p.whole;
@@ -276,12 +278,34 @@ struct SegCursor {
     int s, kh, b, off, len;   // off: work tiles of unit (s, kh, b) already passed
     long long left;
     bool first;
+    int u;                    // whole units: the CTA's next one
+
+    // Sliding windows, whole units: the CTA's next unit with tiles.
+    __device__ __forceinline__ bool next_unit(const WinParams &p)
+    {
+        const int units = p.S * p.Hkv * p.n_rblk;
+        for (; u < units; u += gridDim.x) {
+            int v = u / p.n_rblk;
+            b = u - v * p.n_rblk;
+            s = v / p.Hkv;
+            kh = v - s * p.Hkv;
+            len = __ldg(p.lens + s);
+            left = len_ok(p, len) ? unit_tiles(p, len, b) : 0;
+            if (left > 0) {
+                off = p.VT;
+                u += gridDim.x;
+                return true;
+            }
+        }
+        return false;
+    }
 
     template <class P>
     __device__ __forceinline__ void init(const P &p, const CtaRange &r)
     {
         left = r.g1 - r.g0;
         first = true;
+        u = blockIdx.x + gridDim.x;
         s = r.s0;
         kh = b = off = 0;
         len = 0;
@@ -312,6 +336,10 @@ struct SegCursor {
     template <class P>
     __device__ __forceinline__ bool next(const P &p, WorkItem &w)
     {
+        if constexpr (std::is_same_v<P, WinParams>) {
+            if (left == 0 && p.whole == 1 && !next_unit(p))
+                return false;
+        }
         while (left > 0) {
             const int wu = unit_work(p, len, b);
             const int n = static_cast<int>(min((long long)(wu - off), left));

@@ -144,6 +144,29 @@ bool takes_win_kernel(WinParams &p, int sms, int forced)
     return true;
 }
 
+// How many pieces a sliding-window call on the tensor-core kernels cuts each
+// unit into, one to a CTA (plan.cuh); 0: the work is dealt out evenly.  Dealing
+// out costs every CTA a second start, a walk over all row blocks at both ends
+// and a merge that looks at every row: 2 streams x 4,096 rows of 32 heads over
+// 4,096 positions took 1,236 us that way and take 1,014 in whole units, 16 x 8
+// rows over 512 the same, 28 and 27.  So units that fit the CTAs are always cut
+// into as many pieces as there are CTAs for (56 units of 800 rows over 4,096
+// positions: 55 us, 62 dealt out, 76 whole), and more units stay whole unless
+// the last round would leave more than kIdle tiles per unit to idle CTAs (head
+// dim 128, 80 units more than two rounds hold: 7.7 idle tiles 146 us, dealt out
+// 175; 28 tiles 144 and 120).  Head dims 256 and 512 have longer tiles.
+int32_t window_pieces(const WinParams &p, int64_t units, int64_t cap, int32_t max_len)
+{
+    const int64_t kIdle = p.D == 128 ? 12 : p.D == 256 ? 4 : 2;
+    if (units == 0 || units > INT32_MAX / 2)
+        return 0;
+    const int64_t tiles = head_work(p, max_len) / p.n_rblk - p.VT + 1;
+    if (units <= cap)
+        return static_cast<int32_t>(std::min<int64_t>(cap / units, tiles));
+    const int64_t idle = (units + cap - 1) / cap * cap - units;
+    return idle * tiles <= kIdle * units;
+}
+
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
               int32_t rows_max, bool tree, Plan *plan, const Window *win = nullptr)
 {
@@ -284,19 +307,12 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     // than a few idle SMs (measured on the chunked prompt: 128 units on 148).
     const int64_t units = (int64_t)p.S * p.Hkv * p.n_rblk;
     const int cap = sms < kMaxCtas ? sms : kMaxCtas;
-    if (plan->kernel == Kernel::kPrompt)
+    if (win && plan->kernel != Kernel::kWin)
+        p.whole = window_pieces(p, units, cap, st->max_len);
+    else if (plan->kernel == Kernel::kPrompt)
         p.whole = units <= cap && 4 * units >= 3 * (int64_t)cap;
-    // A sliding-window call on the position-major kernel with fewer units than
-    // CTAs: as many whole pieces per unit as there are CTAs for, if that uses
-    // three quarters of them.
-    if (win && plan->kernel == Kernel::kPm && units > 0 && units <= cap) {
-        const int64_t tiles = head_work(p, st->max_len) / p.n_rblk - p.VT + 1;
-        const int64_t pieces = std::min<int64_t>(cap / units, tiles);
-        if (4 * units * pieces >= 3 * (int64_t)cap || pieces == tiles)
-            p.whole = static_cast<int32_t>(pieces);
-    }
     if (p.whole && plan->kernel != Kernel::kWin)
-        grid = units > 0 ? units * p.whole : 1;
+        grid = std::min<int64_t>(units * p.whole, cap);
     plan->grid = static_cast<int>(grid);
     if (plan->kernel == Kernel::kWin) {
         plan->grid = static_cast<int>(units * p.whole);

@@ -678,13 +678,13 @@ int win_clusters_rows(int D, int C)
 // Blocks per cluster, and what the call then costs (in chunks).  The blocks of
 // one wave run side by side; a block's time is its warps' chunks one after
 // another, plus starting and joining (about kEntry chunks).  So: the cluster
-// size whose waves times that is least (ties to the smaller).  With 96 units
-// and two blocks to an SM, clusters of 3 were 93 at once and a second wave for
-// the other three (68 us against 57 in clusters of 2).
+// size whose waves times that is least (ties to the smaller).
 WinSplit win_split(const WinParams &p, int64_t units)
 {
     constexpr int kEntry = 4;
-    const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + p.W);
+    // (a block's rows span at most so many of the call's)
+    const int span = std::min(p.W, (p.RB + p.G - 2) / p.G + 1);
+    const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + span);
     const int64_t chunks = (seen + kChunk - 1) / kChunk;
     const int teams = kWinWarps / (p.D / 128);
     WinSplit best = {1, INT64_MAX};

@@ -108,42 +108,6 @@ bool pool_rows_past_31_bits(const tf_kv_pool *pool)
     return (int64_t)pool->n_pages * pool->n_kv_heads * pool->page_size > INT32_MAX;
 }
 
-// Row blocks of the position-major or prompt kernel against the cluster kernel
-// (attn_win.cu) for a sliding-window call, by estimates fitted to both kernels
-// over 475 calls (head dims 128, 256 and 512; 8 to 1,600 rows per KV head; 2 to
-// 256 units; windows of 64 to 8,192): the choice is 0.7% slower than the faster
-// of the two in the geometric mean, 27% at worst, where always the cluster
-// kernel up to 16 rows was 21%, never 39%.  In tenths of microseconds:
-//   cluster      its chunks one after another, 1.4 to 2.0 us each: it starts in
-//                about 4 us, but reads the unit again for every 16 rows, and
-//                its products run on mma.sync and FMAs
-//   tensor core  18 to 28 us to start and merge, then 1.6, 2.6 or 4.6 us per
-//                128-position tile, and 6 to 14 per unit
-// Sets p.RB and p.whole for the cluster kernel when it is taken.
-bool takes_win_kernel(WinParams &p, int sms, int forced)
-{
-    const int d = p.D == 128 ? 0 : p.D == 256 ? 1 : 2;
-    WinParams c = p;
-    c.RB = p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;
-    const int64_t heads = (int64_t)p.S * p.Hkv;
-    const int64_t units = heads * ((p.M + c.RB - 1) / c.RB);
-    if (units > INT32_MAX / kMaxCluster)
-        return false;
-    const WinSplit split = win_split(c, units);
-    const int64_t cluster = split.cost < INT64_MAX / 64 ? split.cost * (c.RB <= 8 ? 14 + d : 16 + 2 * d) : INT64_MAX;
-    const int rows = p.D > 128 || p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;  // of its row blocks
-    const int64_t blocks = (p.M + rows - 1) / rows;
-    const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + std::min(p.W, (rows + p.G - 1) / p.G));
-    const int64_t tiles2 = 2 * ((seen + 127) / 128) + 1;  // (half a tile more for the edges)
-    constexpr int kStart[3] = {180, 210, 280}, kTile[3] = {16, 26, 46}, kUnit[3] = {60, 100, 140};
-    const int64_t tensor = kStart[d] + heads * blocks * (tiles2 * kTile[d] / 2 + kUnit[d]) / sms;
-    if (forced == 1 || (forced == 0 && cluster >= tensor))
-        return false;
-    p.RB = c.RB;
-    p.whole = split.C;
-    return true;
-}
-
 // How many pieces a sliding-window call on the tensor-core kernels cuts each
 // unit into, one to a CTA (plan.cuh); 0: the work is dealt out evenly.  Dealing
 // out costs every CTA a second start, a walk over all row blocks at both ends
@@ -154,17 +118,65 @@ bool takes_win_kernel(WinParams &p, int sms, int forced)
 // positions: 55 us, 62 dealt out, 76 whole), and more units stay whole unless
 // the last round would leave more than kIdle tiles per unit to idle CTAs (head
 // dim 128, 80 units more than two rounds hold: 7.7 idle tiles 146 us, dealt out
-// 175; 28 tiles 144 and 120).  Head dims 256 and 512 have longer tiles.
-int32_t window_pieces(const WinParams &p, int64_t units, int64_t cap, int32_t max_len)
+// 175; 28 tiles 144 and 120).  Head dims 256 and 512 have longer tiles.  `tiles`:
+// of a unit at most.
+int32_t window_pieces(int32_t head_dim, int64_t units, int64_t cap, int64_t tiles)
 {
-    const int64_t kIdle = p.D == 128 ? 12 : p.D == 256 ? 4 : 2;
+    const int64_t kIdle = head_dim == 128 ? 12 : head_dim == 256 ? 4 : 2;
     if (units == 0 || units > INT32_MAX / 2)
         return 0;
-    const int64_t tiles = head_work(p, max_len) / p.n_rblk - p.VT + 1;
     if (units <= cap)
         return static_cast<int32_t>(std::min<int64_t>(cap / units, tiles));
     const int64_t idle = (units + cap - 1) / cap * cap - units;
     return idle * tiles <= kIdle * units;
+}
+
+// Row blocks of the position-major or prompt kernel against the cluster kernel
+// (attn_win.cu) for a sliding-window call, by estimates fitted to both kernels
+// over 638 calls (head dims 128, 256 and 512; 8 to 1,600 rows per KV head; 2 to
+// 256 units; windows of 64 to 8,192): the choice is 0.6% slower than the faster
+// of the two in the geometric mean, 28% at worst, where always the cluster
+// kernel up to 16 rows was 11%, never 25%.  In tenths of microseconds, without
+// what both take to start:
+//   cluster      its chunks one after another, 1.2 to 2.1 us each: it reads the
+//                unit again for every 16 rows, and its products run on mma.sync
+//                and FMAs
+//   tensor core  5 to 9 us more to start, then 1.4, 3.3 or 5 us per 128-position
+//                tile that a CTA takes, 11 to 13 per unit, and 20 where the work
+//                is dealt out
+// Sets p.RB and p.whole for the cluster kernel when it is taken.
+bool takes_win_kernel(WinParams &p, int sms, int forced)
+{
+    const int d = p.D == 128 ? 0 : p.D == 256 ? 1 : 2;
+    WinParams c = p;
+    c.RB = p.M <= 4 ? 4 : p.M <= 8 ? 8 : 16;
+    const int64_t heads = (int64_t)p.S * p.Hkv;
+    const int64_t units = heads * ((p.M + c.RB - 1) / c.RB);
+    if (units > INT32_MAX / kMaxCluster)
+        return false;
+    constexpr int kChunk8[3] = {12, 17, 15}, kChunk16[3] = {17, 21, 20};
+    const WinSplit split = win_split(c, units);
+    const int64_t cluster =
+        split.cost < INT64_MAX / 64 ? split.cost * (c.RB <= 8 ? kChunk8 : kChunk16)[d] : INT64_MAX;
+    const int rows = p.D > 128 || p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;  // of its row blocks
+    const int64_t blocks = heads * ((p.M + rows - 1) / rows);
+    const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + std::min(p.W, (rows + p.G - 1) / p.G));
+    const int64_t tiles2 = 2 * ((seen + 127) / 128) + 1;  // (half a tile more for the edges)
+    constexpr int kStart[3] = {80, 50, 90}, kTile[3] = {14, 33, 50}, kUnit[3] = {130, 110, 130};
+    constexpr int kDealt = 200;
+    const int64_t pieces = window_pieces(p.D, blocks, sms, (tiles2 + 1) / 2);
+    int64_t tensor = kStart[d];
+    if (pieces == 0)
+        tensor += kDealt + blocks * (tiles2 * kTile[d] / 2 + kUnit[d]) / sms;
+    else if (pieces > 1)
+        tensor += ((tiles2 + 1) / 2 + pieces - 1) / pieces * kTile[d] + kUnit[d];
+    else
+        tensor += (blocks + sms - 1) / sms * (tiles2 * kTile[d] / 2 + kUnit[d]);
+    if (forced == 1 || (forced == 0 && cluster >= tensor))
+        return false;
+    p.RB = c.RB;
+    p.whole = split.C;
+    return true;
 }
 
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
@@ -308,7 +320,7 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     const int64_t units = (int64_t)p.S * p.Hkv * p.n_rblk;
     const int cap = sms < kMaxCtas ? sms : kMaxCtas;
     if (win && plan->kernel != Kernel::kWin)
-        p.whole = window_pieces(p, units, cap, st->max_len);
+        p.whole = window_pieces(p.D, units, cap, head_work(p, st->max_len) / p.n_rblk - p.VT + 1);
     else if (plan->kernel == Kernel::kPrompt)
         p.whole = units <= cap && 4 * units >= 3 * (int64_t)cap;
     if (p.whole && plan->kernel != Kernel::kWin)

@@ -231,14 +231,15 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
         const int n = (it.key1 - it.key0 + PT - 1) / PT;
         const int m = it.b * RR + r;
         const bool live = m < p.M;
+        size_t row;  // the row's output (and query) row
         // --- the row's query into tensor memory (each half thread its 64
         // dims); the row's output offset ---------------------------------------
         {
             const int mm = min(m, p.M - 1);
             const int wr = mm / p.G;
             const int h = it.kh * p.G + (mm - wr * p.G);
-            const size_t row = ((size_t)it.s * p.W + wr) * p.Hq + h;
-            if (hh == 0)
+            row = ((size_t)it.s * p.W + wr) * p.Hq + h;
+            if (!kWin && hh == 0)
                 sm.rowoff[r] = live ? (int)row : -1;
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * DD + 64 * hh);
             uint32_t qr[32];
@@ -329,6 +330,12 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
             // a half that would move the row's reference calls for the slow path
             const bool hgrow = hm != NEG_INF && (mref == NEG_INF || hm > mref + kRescaleLog2);
             [[maybe_unused]] bool moved = false;  // (long sliding windows: used below)
+            if constexpr (kWin) {
+                // (the last segment's rows have left the P tile; the vote orders the
+                // other threads' writes to it)
+                if (t == 0)
+                    bulk_wait_read<0>();
+            }
             if (block_any<256>(hgrow)) {
                 // the row's tile max from its two halves; both threads of the
                 // row take the same decision from the same values
@@ -469,43 +476,86 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
         named_barrier(1, 256);
         const bool write = ok && !sm.abort_flag;
         float *slot = it.fin ? nullptr : p.part + (size_t)it.slot * part_slot_floats(p);
-        // O^T lane r is head dim r; this thread takes rows [64 hh, 64 hh + 64)
+        if constexpr (kWin) {
+            // The rows go through the P tile, whose last PV is complete, and leave
+            // it by bulk copies of 512 bytes while the next segment starts: a
+            // window's segments are short, and storing the rows from here took 8
+            // to 10 us of each (2 streams x 4,096 rows over 4,096 positions:
+            // 1,024 us).
+            float(*const stage)[DD] = reinterpret_cast<float(*)[DD]>(sm.pbuf);
+            if (hh == 0)
+                sm.alpha[r] = it.fin ? 1.f / (sm.lhalf[0][r] + sm.lhalf[1][r]) : 1.f;
+            named_barrier(1, 256);
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-            const int r0 = 64 * hh + 32 * c;
-            uint32_t hi[32], lo[32];
-            tmem_ld32(lane_base + kColO + r0, hi);
-            tmem_ld32(lane_base + kColO + RR + r0, lo);
-            tmem_wait_ld();
-            if (kFold && n <= kFoldTiles) {  // nothing was folded
+            for (int c = 0; c < 2; ++c) {
+                const int r0 = 64 * hh + 32 * c;
+                uint32_t hi[32], lo[32];
+                tmem_ld32(lane_base + kColO + r0, hi);
+                if (!kFold || n > kFoldTiles)
+                    tmem_ld32(lane_base + kColO + RR + r0, lo);
+                tmem_wait_ld();
+                if (kFold && n <= kFoldTiles) {  // nothing was folded
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    lo[e] = 0u;
+                    for (int e = 0; e < 32; ++e)
+                        lo[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(&sm.alpha[r0 + e]);
+                    stage[r0 + e][r] = (__uint_as_float(hi[e]) + __uint_as_float(lo[e])) * k.x;
+                    stage[r0 + e + 1][r] = (__uint_as_float(hi[e + 1]) + __uint_as_float(lo[e + 1])) * k.y;
+                    stage[r0 + e + 2][r] = (__uint_as_float(hi[e + 2]) + __uint_as_float(lo[e + 2])) * k.z;
+                    stage[r0 + e + 3][r] = (__uint_as_float(hi[e + 3]) + __uint_as_float(lo[e + 3])) * k.w;
+                }
             }
-            if (write) {
+            fence_async_smem();
+            named_barrier(1, 256);
+            if (write && hh == 0 && (it.fin ? live : r < p.SR)) {
+                bulk_s2g(it.fin ? p.out + row * DD : slot + (size_t)r * DD, stage[r], DD * 4);
+                bulk_commit();
+                if (!it.fin) {
+                    slot[(size_t)p.SR * DD + r] = mref;
+                    slot[(size_t)p.SR * DD + p.SR + r] = sm.lhalf[0][r] + sm.lhalf[1][r];
+                }
+            }
+        } else {
+            // O^T lane r is head dim r; this thread takes rows [64 hh, 64 hh + 64)
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                const int r0 = 64 * hh + 32 * c;
+                uint32_t hi[32], lo[32];
+                tmem_ld32(lane_base + kColO + r0, hi);
+                tmem_ld32(lane_base + kColO + RR + r0, lo);
+                tmem_wait_ld();
+                if (write) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int rr = r0 + e;
-                    const float o = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
-                    if (it.fin) {
-                        const int orow = sm.rowoff[rr];
-                        if (orow >= 0)
-                            p.out[(size_t)orow * DD + r] = o / (sm.lhalf[0][rr] + sm.lhalf[1][rr]);
-                    } else if (rr < p.SR) {
-                        slot[(size_t)rr * DD + r] = o;
+                    for (int e = 0; e < 32; ++e) {
+                        const int rr = r0 + e;
+                        const float o = __uint_as_float(hi[e]) + __uint_as_float(lo[e]);
+                        if (it.fin) {
+                            const int orow = sm.rowoff[rr];
+                            if (orow >= 0)
+                                p.out[(size_t)orow * DD + r] = o / (sm.lhalf[0][rr] + sm.lhalf[1][rr]);
+                        } else if (rr < p.SR) {
+                            slot[(size_t)rr * DD + r] = o;
+                        }
                     }
                 }
             }
-        }
-        if (write && !it.fin && hh == 0 && r < p.SR) {
-            slot[(size_t)p.SR * DD + r] = mref;
-            slot[(size_t)p.SR * DD + p.SR + r] = sm.lhalf[0][r] + sm.lhalf[1][r];
+            if (write && !it.fin && hh == 0 && r < p.SR) {
+                slot[(size_t)p.SR * DD + r] = mref;
+                slot[(size_t)p.SR * DD + p.SR + r] = sm.lhalf[0][r] + sm.lhalf[1][r];
+            }
         }
         tc_fence_before();
-        // every thread is done with rowoff / lhalf before the next segment writes them
-        named_barrier(1, 256);
+        // every thread is done with rowoff / lhalf before the next segment writes
+        // them (sliding windows: the barrier above)
+        if constexpr (!kWin)
+            named_barrier(1, 256);
         u0 += n;
     }
+    if constexpr (kWin)
+        bulk_wait_all();
 }
 
 // kWin: sliding windows.  kFold: long ones, whose O^T is folded into a second

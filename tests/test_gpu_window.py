@@ -204,6 +204,31 @@ def test_lengths_out_of_range_and_bad_pages_are_reported():
     assert tf.tf_workspace_status(ws) & tf.TF_DEV_BAD_PAGE
 
 
+@pytest.mark.parametrize("d,G,rows,S,Hkv", [(128, 4, 300, 20, 2), (128, 8, 8, 170, 1), (128, 4, 40, 3, 2), (128, 2, 70, 300, 1),
+                                           (256, 4, 8, 160, 1), (512, 4, 8, 5, 3), (512, 8, 4, 300, 1)])
+@pytest.mark.parametrize("kernel", [0, TENSOR_CORE, CLUSTER])
+def test_units_of_streams_out_of_range_among_others(d, G, rows, S, Hkv, kernel):
+    """Fewer units than the GPU has CTAs, more, and many more; some streams too
+    long, one too short, one of just the call's rows.  Nothing past the output
+    is written."""
+    import verify_paged_gqa_b200 as tf
+    lens = [rows + (53 * i) % 400 for i in range(S)]
+    c = WindowCase(lens, rows, 90, 4, d=d, G=G, P=64, Hkv=Hkv, seed=S + d)
+    bad = {0: 2000, S // 2: rows - 1, S - 1: -5}
+    for s, n in bad.items():
+        c.lens[s] = n
+    flat = torch.full((c.q.numel() + 4096,), 7.0, dtype=torch.float32, device="cuda")
+    out, ws = flat[:c.q.numel()].view(c.q.shape), big_workspace()
+    tf.tf_testing_paged_attn_window(c.k_pool, c.v_pool, c.table, c.lens, c.q, 90, 4, c.scale, out, ws, c.max_len, kernel=kernel)
+    assert tf.tf_workspace_status(ws) == tf.TF_DEV_BAD_LEN
+    assert bool((flat[c.q.numel():] == 7.0).all())
+    for s in bad:
+        assert torch.isnan(out[s]).all()
+    for s in set(range(S)) - set(bad):
+        ref, bound = window_ref.attend(c.q[s], c.k[s], c.v[s], 90, 4, c.scale)
+        assert ((out[s].double() - ref).abs() <= bound).all(), s
+
+
 def test_refusals_that_need_the_device():
     import verify_paged_gqa_b200 as tf
     c = WindowCase([900, 1500], 1, 200, 4, P=64, seed=9)

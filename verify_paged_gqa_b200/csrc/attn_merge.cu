@@ -16,7 +16,9 @@
 // warp per row.  A row's first round of O loads and its (m, l) loads are all
 // in flight together.  The kernel is launched as a programmatic dependent of
 // the partial kernel, so its launch overlaps that kernel's last CTAs.
-// Streams whose length is out of range get NaN rows (and the status bit).
+// Streams whose length is out of range get NaN rows (and the status bit); a
+// sliding-window call whose units were all finished whole launches a block per
+// stream for that alone (a block per row group took 140 us of a 1,240 us call).
 #include "launch.cuh"
 #include "plan.cuh"
 

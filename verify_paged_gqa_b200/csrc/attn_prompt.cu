@@ -19,6 +19,13 @@
 // epilogue adds.  16 instructions per tile instead of 24 for a row-major PV
 // run once per half.
 //
+// Sliding windows (kWin): the same products over the squeezed positions of
+// plan.cuh.  P's parts are rounded to nearest instead (2^-18 of P, no bias), a
+// CTA takes whole row blocks, and their rows leave through shared memory while
+// the next block starts.  2 streams x 4,096 rows of 32 heads over a window of
+// 4,096: 928 us, 593 TFLOP/s of the products that the rows see; a tile takes
+// 1.5 us of it, a block beside its tiles 13 to 16.
+//
 // One persistent CTA per SM, ten warps:
 //   warp 0     producer (one lane): the K/V ring (ring.cuh).
 //   warp 1     MMA issuer (one lane): QK(t + 1) before PV(t).  S has one
@@ -382,16 +389,16 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                     ok = pwait(sm, &sm.o_done, (u - 1) & 1u, p.flags, kWaitEmpty) && ok;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t ta = lane_base + kColO + 64 * hh + 32 * c, tf = ta + RR;
-                        const float *al = &sm.alpha[64 * hh + 32 * c];
-                        uint32_t v[32], f[32];
-                        tmem_ld32(ta, v);
+                    for (int c = 0; c < 4; ++c) {  // (16 columns: the scores stay in registers)
+                        const uint32_t ta = lane_base + kColO + 64 * hh + 16 * c, tf = ta + RR;
+                        const float *al = &sm.alpha[64 * hh + 16 * c];
+                        uint32_t v[16], f[16];
+                        tmem_ld16(ta, v);
                         if (t > kFoldTiles)  // (folded sums exist from the first fold on)
-                            tmem_ld32(tf, f);
+                            tmem_ld16(tf, f);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float k = moved ? al[e] : 1.f;
                             float x = __uint_as_float(v[e]) * k;
                             float y = t > kFoldTiles ? __uint_as_float(f[e]) * k : 0.f;
@@ -400,9 +407,9 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
                             f[e] = __float_as_uint(y);
                         }
                         if (!fold)
-                            tmem_st32(ta, v);
+                            tmem_st16(ta, v);
                         if (fold || t > kFoldTiles)
-                            tmem_st32(tf, f);
+                            tmem_st16(tf, f);
                     }
                     tmem_wait_st();
                 }
@@ -479,9 +486,9 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
         if constexpr (kWin) {
             // The rows go through the P tile, whose last PV is complete, and leave
             // it by bulk copies of 512 bytes while the next segment starts: a
-            // window's segments are short, and storing the rows from here took 8
-            // to 10 us of each (2 streams x 4,096 rows over 4,096 positions:
-            // 1,024 us).
+            // window's segments are short, and storing the rows from here took
+            // 7 us of each (2 streams x 4,096 rows over 4,096 positions: 1,024 us
+            // in place of 928; over 128 positions 312 in place of 233).
             float(*const stage)[DD] = reinterpret_cast<float(*)[DD]>(sm.pbuf);
             if (hh == 0)
                 sm.alpha[r] = it.fin ? 1.f / (sm.lhalf[0][r] + sm.lhalf[1][r]) : 1.f;
@@ -668,8 +675,8 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t strea
 
 // Sliding windows start and end inside tiles: pieces at any page size.  Windows
 // of more than kFoldWindow positions fold: 2 streams x 4,096 rows x 32 heads
-// over 4,096 positions take 1,303 us without and 1,548 with, off by 5e-6 and
-// 3e-6 of the output's norm; over 8,192 it would be 8e-6 without, and growing.
+// over 4,096 positions take 928 us without and 1,241 with, off by 5e-6 and 3e-6
+// of the output's norm; over 8,192 it would be 8e-6 without, and growing.
 constexpr int kFoldWindow = 4608;
 
 cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream)

@@ -23,9 +23,10 @@
 // the same arithmetic and combines them in position order.  (When the call's
 // units fill most CTAs but not more, the tensor-bound prompt kernel instead
 // gives CTA c unit c whole: no partials and no merge.  A sliding-window call
-// with fewer units than CTAs cuts each unit into the same number of pieces,
-// one to a CTA: its units are short, and a CTA whose range crossed into a
-// second one would pay two starts on the call's critical path.)  A unit's result
+// cuts each unit into the same number of pieces, one to a CTA, or where there
+// are more units than CTAs gives every CTA whole ones in turn: its units are
+// short, and a CTA whose range crossed into a second one would pay two starts on
+// the call's critical path.)  A unit's result
 // therefore depends on the lengths of the call's streams and the grid size
 // (never on the page table, nor on run-to-run timing).
 //

@@ -111,15 +111,15 @@ bool pool_rows_past_31_bits(const tf_kv_pool *pool)
 // How many pieces a sliding-window call on the tensor-core kernels cuts each
 // unit into, one to a CTA (plan.cuh); 0: the work is dealt out evenly.  Dealing
 // out costs every CTA a second start, a walk over all row blocks at both ends
-// and a merge that looks at every row: 2 streams x 4,096 rows of 32 heads over
-// 4,096 positions took 1,236 us that way and take 1,014 in whole units, 16 x 8
-// rows over 512 the same, 28 and 27.  So units that fit the CTAs are always cut
-// into as many pieces as there are CTAs for (56 units of 800 rows over 4,096
-// positions: 55 us, 62 dealt out, 76 whole), and more units stay whole unless
-// the last round would leave more than kIdle tiles per unit to idle CTAs (head
-// dim 128, 80 units more than two rounds hold: 7.7 idle tiles 146 us, dealt out
-// 175; 28 tiles 144 and 120).  Head dims 256 and 512 have longer tiles.  `tiles`:
-// of a unit at most.
+// and a merge that looks at every row.  So units that fit the CTAs are cut into
+// as many pieces as there are CTAs for (8 units of seven row blocks over 4,096
+// positions: 53 us, dealt out 59, whole 72), and more units stay whole (2
+// streams x 4,096 rows of 32 heads over 4,096 positions: 925 us, dealt out
+// 1,128; over 1,024: 419 and 608), unless the last round would leave more than
+// kIdle tiles per unit to idle CTAs (64 rows over 4,096 positions at head dim
+// 128: 240 units, 8 idle tiles, 147 us and dealt out 176; 160 units, 28 idle
+// tiles, 145 and 119).  Head dims 256 and 512 have longer tiles.  `tiles`: of a
+// unit at most.
 int32_t window_pieces(int32_t head_dim, int64_t units, int64_t cap, int64_t tiles)
 {
     const int64_t kIdle = head_dim == 128 ? 12 : head_dim == 256 ? 4 : 2;

@@ -376,7 +376,10 @@ TF_API int tf_paged_attn_prompt(const tf_kv_pool *pool, const tf_streams *stream
  * dim, ratio of heads and page size.  Table entries and pool slots of
  * positions that no row of the call sees are never read: pages wholly behind
  * the window (tf_kv_pages_free_window) may hold -1 or belong to somebody
- * else.  TF_EUNSUPPORTED for pools of more than 2^31 - 1 rows (n_pages *
+ * else.  A position that some rows of the call see and others do not is
+ * masked by its score: its K may be anything to the others, but a V value
+ * that is infinite or NaN can reach every row of the call, as in the other
+ * calls.  TF_EUNSUPPORTED for pools of more than 2^31 - 1 rows (n_pages *
  * n_kv_heads * page_size).  The workspace is sized by its own call, since a
  * window may be split over other kernels than the whole context; one
  * workspace of the larger size serves both kinds of layer in turn. */

@@ -262,6 +262,29 @@ def test_a_captured_call_follows_the_lengths():
     assert tf.tf_workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("d,G,rows,S,Hkv", [(128, 4, 40, 3, 2), (128, 4, 120, 30, 2), (128, 8, 8, 160, 1), (512, 4, 8, 5, 3)])
+def test_captured_tensor_core_calls_follow_the_lengths(d, G, rows, S, Hkv):
+    """Units in pieces and whole ones, replayed with shorter streams."""
+    import verify_paged_gqa_b200 as tf
+    c = WindowCase([500 + rows + (29 * i) % 300 for i in range(S)], rows, 400, 4, d=d, G=G, P=64, Hkv=Hkv, seed=d + S)
+    c.window = 300   # the pool holds 100 positions more than the calls see
+    out, ws = torch.empty(c.q.shape, dtype=torch.float32, device="cuda"), big_workspace()
+    call = lambda: tf.tf_testing_paged_attn_window(c.k_pool, c.v_pool, c.table, c.lens, c.q, 300, 4, c.scale, out, ws, c.max_len, kernel=TENSOR_CORE)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    full = (c.lens.clone(), c.k, c.v)
+    for back in (0, 1, 64, 99):
+        c.lens.copy_(full[0] - back)
+        c.k, c.v = ([t[:len(t) - back] for t in kv] for kv in full[1:])
+        out.fill_(float("nan"))
+        graph.replay()
+        c.check(out)
+    assert tf.tf_workspace_status(ws) == 0
+
+
 def test_another_stream_and_two_workspaces():
     a = WindowCase([2000, 900], 8, 500, 4, G=8, seed=21)
     b = WindowCase([1800, 400], 1, 700, 0, d=256, seed=22)

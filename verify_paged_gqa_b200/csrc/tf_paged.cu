@@ -136,14 +136,16 @@ int32_t window_pieces(int32_t head_dim, int64_t units, int64_t cap, int64_t tile
 // over 638 calls (head dims 128, 256 and 512; 8 to 1,600 rows per KV head; 2 to
 // 256 units; windows of 64 to 8,192): the choice is 0.6% slower than the faster
 // of the two in the geometric mean, 28% at worst, where always the cluster
-// kernel up to 16 rows was 11%, never 25%.  In tenths of microseconds, without
+// kernel up to 16 rows was 11%, never 25%.  Over 400 others, drawn over all page
+// sizes and ratios of heads, it was 0.5% (55% for one, over pages of 16).  In tenths of microseconds, without
 // what both take to start:
 //   cluster      its chunks one after another, 1.2 to 2.1 us each: it reads the
 //                unit again for every 16 rows, and its products run on mma.sync
 //                and FMAs
 //   tensor core  5 to 9 us more to start, then 1.4, 3.3 or 5 us per 128-position
-//                tile that a CTA takes, 11 to 13 per unit, and 20 where the work
-//                is dealt out
+//                tile that a CTA takes (twice that over pages below 32 positions
+//                at head dims 256 and 512: copies by the piece), 11 to 13 per
+//                unit, and 20 where the work is dealt out
 // Sets p.RB and p.whole for the cluster kernel when it is taken.
 bool takes_win_kernel(WinParams &p, int sms, int forced)
 {
@@ -154,24 +156,27 @@ bool takes_win_kernel(WinParams &p, int sms, int forced)
     const int64_t units = heads * ((p.M + c.RB - 1) / c.RB);
     if (units > INT32_MAX / kMaxCluster)
         return false;
-    constexpr int kChunk8[3] = {12, 17, 15}, kChunk16[3] = {17, 21, 20};
+    constexpr int kChunk4 = 12, kChunk8[3] = {12, 17, 15}, kChunk16[3] = {17, 21, 20};
     const WinSplit split = win_split(c, units);
     const int64_t cluster =
-        split.cost < INT64_MAX / 64 ? split.cost * (c.RB <= 8 ? kChunk8 : kChunk16)[d] : INT64_MAX;
+        split.cost < INT64_MAX / 64
+            ? split.cost * (c.RB == 4 ? kChunk4 : c.RB == 8 ? kChunk8[d] : kChunk16[d])
+            : INT64_MAX;
     const int rows = p.D > 128 || p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;  // of its row blocks
     const int64_t blocks = heads * ((p.M + rows - 1) / rows);
     const int64_t seen = std::min<int64_t>(p.max_len, (int64_t)p.window + p.sinks + std::min(p.W, (rows + p.G - 1) / p.G));
     const int64_t tiles2 = 2 * ((seen + 127) / 128) + 1;  // (half a tile more for the edges)
     constexpr int kStart[3] = {80, 50, 90}, kTile[3] = {14, 33, 50}, kUnit[3] = {130, 110, 130};
+    const int64_t tile = p.P < 32 && p.D > 128 ? 2 * kTile[d] : kTile[d];
     constexpr int kDealt = 200;
     const int64_t pieces = window_pieces(p.D, blocks, sms, (tiles2 + 1) / 2);
     int64_t tensor = kStart[d];
     if (pieces == 0)
-        tensor += kDealt + blocks * (tiles2 * kTile[d] / 2 + kUnit[d]) / sms;
+        tensor += kDealt + blocks * (tiles2 * tile / 2 + kUnit[d]) / sms;
     else if (pieces > 1)
-        tensor += ((tiles2 + 1) / 2 + pieces - 1) / pieces * kTile[d] + kUnit[d];
+        tensor += ((tiles2 + 1) / 2 + pieces - 1) / pieces * tile + kUnit[d];
     else
-        tensor += (blocks + sms - 1) / sms * (tiles2 * kTile[d] / 2 + kUnit[d]);
+        tensor += (blocks + sms - 1) / sms * (tiles2 * tile / 2 + kUnit[d]);
     if (forced == 1 || (forced == 0 && cluster >= tensor))
         return false;
     p.RB = c.RB;

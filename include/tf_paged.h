@@ -37,7 +37,8 @@
  *  j % page_size.  Query head h reads KV head h / (n_q_heads / n_kv_heads).
  *
  *  The output is softmax(scale * q . k) weighted sum of v, accumulated in
- *  fp32 from bf16 inputs.  Which pool pages hold a stream's positions never
+ *  fp32 from bf16 inputs; scale is any finite number (TF_EINVAL otherwise),
+ *  zero and negative ones included.  Which pool pages hold a stream's positions never
  *  changes a bit of the result: the arithmetic depends only on positions,
  *  lens, rows and the host arguments.
  *

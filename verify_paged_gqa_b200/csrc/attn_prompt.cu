@@ -90,9 +90,13 @@ static_assert(kPrSmemBytes <= 232448, "shared memory");
 
 // Kernel arguments: the call's parameters and the K and V pools' tensor maps
 // (one 128-row box, or for tiles assembled from pages one map per box height).
+// The softmax takes a row's maximum over raw scores and masks them with -inf
+// before it scales them, so the scale it sees is positive: a negative one is
+// the queries' sign (q_flip), and one of zero queries of zero (q_keep).
 template <bool kG, class P>
 struct PrArgs {
     P p;
+    uint32_t q_keep, q_flip;  // a pair of query values is taken as (pair & q_keep) ^ q_flip
     CUtensorMap kmap[kG ? kBoxHeights : 1];
     CUtensorMap vmap[kG ? kBoxHeights : 1];
 };
@@ -253,10 +257,10 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                qr[c * 4 + 0] = v.x;
-                qr[c * 4 + 1] = v.y;
-                qr[c * 4 + 2] = v.z;
-                qr[c * 4 + 3] = v.w;
+                qr[c * 4 + 0] = (v.x & a.q_keep) ^ a.q_flip;
+                qr[c * 4 + 1] = (v.y & a.q_keep) ^ a.q_flip;
+                qr[c * 4 + 2] = (v.z & a.q_keep) ^ a.q_flip;
+                qr[c * 4 + 3] = (v.w & a.q_keep) ^ a.q_flip;
             }
             // (the previous segment's last QK: complete in practice, its S was read)
             ok = pwait(sm, &sm.q_free, (j & 1u) ^ 1u, p.flags, kWaitQEmpty) && ok;
@@ -649,6 +653,9 @@ cudaError_t launch_prompt(const P &p, int grid, cudaStream_t stream)
 {
     PrArgs<kG, P> a;
     a.p = p;
+    a.q_keep = p.scale_log2 != 0.f ? 0xffffffffu : 0u;
+    a.q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    a.p.scale_log2 = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
     // one box of a whole 128-position tile, or boxes of 1, 2, 4, ..., 128 rows
     // for tiles assembled from page pieces
     for (int h = 0; h < (kG ? kBoxHeights : 1); ++h) {

@@ -383,7 +383,10 @@ TF_API int tf_paged_attn_prompt(const tf_kv_pool *pool, const tf_streams *stream
  * calls.  TF_EUNSUPPORTED for pools of more than 2^31 - 1 rows (n_pages *
  * n_kv_heads * page_size).  The workspace is sized by its own call, since a
  * window may be split over other kernels than the whole context; one
- * workspace of the larger size serves both kinds of layer in turn. */
+ * workspace of the larger size serves both kinds of layer in turn.  The figure
+ * grows with n_streams and with rows * n_q_heads and does not depend on
+ * max_len, window or sinks: taken for the largest of each, it holds for every
+ * smaller call over the same pool.  A smaller workspace is TF_ENOSPACE. */
 TF_API size_t tf_paged_attn_window_workspace_bytes(const tf_kv_pool *pool,
                                                    const tf_streams *streams,
                                                    int32_t n_q_heads, int32_t rows,

@@ -43,8 +43,7 @@ TF_API int tf_testing_paged_attn(const tf_kv_pool *pool, const tf_streams *strea
  * [1, 4096]) with the same two settings and a choice of kernel: 0 the
  * library's own, 1 the tensor-core kernels, 2 the cluster kernel (which waits
  * on no barrier that could be withheld), so that each kernel can be tested at
- * sizes the library gives to the other.  The workspace may have to be larger
- * than tf_paged_attn_window_workspace_bytes says (TF_ENOSPACE). */
+ * sizes the library gives to the other. */
 TF_API int tf_testing_paged_attn_window(const tf_kv_pool *pool, const tf_streams *streams,
                                         const void *q, int32_t n_q_heads, int32_t rows,
                                         int32_t window, int32_t sinks, float scale, float *out,

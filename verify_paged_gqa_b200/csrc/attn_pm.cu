@@ -1122,7 +1122,7 @@ int pm_rows(const AttnParams &p)
     if (p.D == 128)
         return p.M <= 32 ? 32 : (p.M <= 64 || p.has_tree) ? 64 : 0;
     if (p.D == 256 || p.D == 512)
-        return 32;
+        return kPmWideRows;
     return 0;
 }
 

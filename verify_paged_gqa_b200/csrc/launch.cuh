@@ -167,7 +167,9 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t strea
 cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream);
 
 // Position-major tensor-core partial kernel: key positions on the MMA's M,
-// row blocks of pm_rows(p) rows (0: not supported for these arguments).
+// row blocks of pm_rows(p) rows (0: not supported for these arguments),
+// kPmWideRows at head dims 256 and 512.
+constexpr int kPmWideRows = 32;
 int pm_rows(const AttnParams &p);
 cudaError_t launch_attn_pm(const AttnParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_attn_pm(const WinParams &p, int grid, cudaStream_t stream);

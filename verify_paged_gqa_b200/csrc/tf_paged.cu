@@ -72,6 +72,17 @@ size_t ws_part_offset(int S)
     return kWsHeaderBytes + (((size_t)S * 8 + 255) / 256) * 256;
 }
 
+// What every attention call of at most p.S streams and p.M rows per (stream, KV
+// head) fits into, whichever kernel it takes and however short it is: two slots
+// for each of `cap` CTAs, of as many rows as a row block of the head dim can
+// have.  It grows with S and M and depends on nothing else of the call, so the
+// figure for the largest shape serves the smaller ones.
+size_t ws_bytes_of_any(AttnParams p, int cap)
+{
+    p.SR = std::min(p.M, p.D == 128 ? prompt_rows() : kPmWideRows);
+    return ws_part_offset(p.S) + (size_t)2 * cap * part_slot_floats(p) * sizeof(float);
+}
+
 // Entry tiles per unit (plan.cuh), measured: at head dim 512 a unit start
 // costs about 8 tiles' worth of streaming (the ring holds less than one
 // tile, so the pipeline drains and refills); the prompt kernel's split
@@ -330,14 +341,10 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         p.whole = units <= cap && 4 * units >= 3 * (int64_t)cap;
     if (p.whole && plan->kernel != Kernel::kWin)
         grid = std::min<int64_t>(units * p.whole, cap);
-    plan->grid = static_cast<int>(grid);
-    if (plan->kernel == Kernel::kWin) {
-        plan->grid = static_cast<int>(units * p.whole);
-        plan->ws_bytes = kWsHeaderBytes;
-        return TF_OK;
-    }
+    plan->grid = static_cast<int>(plan->kernel == Kernel::kWin ? units * p.whole : grid);
     p.n_cta = plan->grid;
-    plan->ws_bytes = ws_part_offset(p.S) + (size_t)2 * plan->grid * part_slot_floats(p) * sizeof(float);
+    plan->ws_bytes = win ? ws_bytes_of_any(p, cap)
+                         : ws_part_offset(p.S) + (size_t)2 * plan->grid * part_slot_floats(p) * sizeof(float);
     return TF_OK;
 }
 

@@ -81,7 +81,7 @@ extern "C" {
 #define TF_OK 0
 #define TF_EINVAL 1        /* a NULL pointer, a bad size or an inconsistent shape */
 #define TF_EUNSUPPORTED 2  /* a shape this library has no kernel for (head_dim, page_size) */
-#define TF_ENOSPACE 3      /* the workspace is smaller than tf_paged_attn_workspace_bytes */
+#define TF_ENOSPACE 3      /* the workspace (or list) is too small for the call */
 #define TF_ECUDA 4         /* a CUDA launch or query failed */
 
 /* Bits of the device-side status word (tf_workspace_status). */
@@ -304,10 +304,12 @@ TF_API int tf_kv_pages_move(const tf_kv_pool *pool, const void *moves, size_t mo
  * owned by the caller, sized once from the largest shape it will run and
  * reused across steps (the DsaSelectScratch doc comment), and a call whose
  * plan needs more than was given fails before any launch instead of
- * overrunning it (DsaSelectScratch::fits; here TF_ENOSPACE).  The figure is
- * for any of the attention calls
- * with these arguments (tf_paged_attn_verify_tree included).  The workspace holds split-context
- * partial results and, in its first 4 bytes, the device status word, which
+ * overrunning it (DsaSelectScratch::fits; here TF_ENOSPACE).  The figure
+ * holds for any of the attention calls with these arguments
+ * (tf_paged_attn_verify_tree included) and for every call over the same pool
+ * with no more n_streams and rows * n_q_heads, of any length; a call refuses
+ * only what it does not fit into.  The workspace holds split-context partial
+ * results and, in its first 4 bytes, the device status word, which
  * the calls only OR bits into: zero those 4 bytes once after allocating
  * (cudaMemset, or one tf_workspace_status call).  The rest needs no
  * initialisation.  One workspace may serve later calls on the same stream;
@@ -416,7 +418,7 @@ TF_API int tf_paged_attn_prompt_window(const tf_kv_pool *pool, const tf_streams 
  * this library, held by every GPU that loads it until the process exits.
  * Arguments, results and errors are those of tf_paged_attn_decode, except:
  *  - TF_ENOSPACE when the call would need more than the 8 MiB of scratch
- *    (tf_paged_attn_workspace_bytes with rows = 1 gives the need);
+ *    (never where tf_paged_attn_workspace_bytes with rows = 1 is at most that);
  *  - the first call on each device looks the array's device address up
  *    (cudaGetSymbolAddress) with that device current; make that first call
  *    before any stream capture on the device;

@@ -61,3 +61,41 @@ def test_smaller_window_calls_run_in_it(d, P, most, calls):
                 for w in (ws, big)]
         assert torch.isfinite(outs[0]).all() and torch.equal(*outs), (S, rows)
     assert tf.tf_workspace_status(ws) == 0
+
+
+def plain_bytes(d, Hkv, G, S, rows, max_len, P=512):
+    import verify_paged_gqa_b200._abi as lib
+    pool = lib.tf_kv_pool(PTR, PTR, 64, Hkv, P, d)
+    st = lib.tf_streams(PTR, -(-max_len // P), PTR, S, max_len)
+    n = lib.raw.tf_paged_attn_workspace_bytes(ctypes.byref(pool), ctypes.byref(st), Hkv * G, rows)
+    assert n > 0
+    return n
+
+
+@pytest.mark.parametrize("d", [128, 256, 512])
+@pytest.mark.parametrize("Hkv,G", [(2, 8), (8, 4), (3, 5)])
+@pytest.mark.parametrize("rows", [1, 8, 448, 1000])
+def test_workspace_of_the_largest_shape_holds_every_smaller_one(d, Hkv, G, rows):
+    most = plain_bytes(d, Hkv, G, 16, rows, 9000)
+    for S, r, n in itertools.product((1, 2, 4, 9, 16), sorted({1, 2, 8, 60, rows // 2 or 1, rows}), (rows, 300, 2048, 9000)):
+        if r <= rows and n >= r:
+            assert plain_bytes(d, Hkv, G, S, r, n) <= most, (S, r, n)
+
+
+def test_a_shorter_prompt_chunk_runs_in_the_workspace_of_a_longer_one():
+    """112 row blocks of 128 rows are taken whole, one to a CTA; 104 are split
+    over all CTAs, whose partials take more room."""
+    import verify_paged_gqa_b200 as tf
+    Hkv, G, L = 8, 4, 2048
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    kp, vp = r(4, Hkv, 512, 128), r(4, Hkv, 512, 128)
+    table, lens = torch.tensor([[2, 0, 3, 1]], dtype=torch.int32, device="cuda"), torch.tensor([L], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(tf.tf_paged_attn_workspace_bytes(kp, vp, table, lens, Hkv * G, 14 * 32, L), dtype=torch.uint8, device="cuda")
+    for rows in (14 * 32, 13 * 32, 100, 9, 4, 1):
+        q = r(1, rows, Hkv * G, 128)
+        fn = tf.tf_paged_attn_decode if rows == 1 else tf.tf_paged_attn_verify if rows <= 8 else tf.tf_paged_attn_prompt
+        out = fn(kp, vp, table, lens, q, 128 ** -0.5, torch.empty(q.shape, dtype=torch.float32, device="cuda"), ws, L)
+        assert torch.isfinite(out).all(), rows
+    assert tf.tf_workspace_status(ws) == 0

@@ -110,7 +110,8 @@ struct Window {
 struct Plan {
     WinParams p;  // a plain call launches its AttnParams part
     int grid;
-    size_t ws_bytes;
+    size_t ws_bytes;  // this call's need
+    size_t ws_any;    // that of any call of its size or less
     Kernel kernel;  // which partial kernel runs the call
 };
 
@@ -343,7 +344,9 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         grid = std::min<int64_t>(units * p.whole, cap);
     plan->grid = static_cast<int>(plan->kernel == Kernel::kWin ? units * p.whole : grid);
     p.n_cta = plan->grid;
-    plan->ws_bytes = win ? ws_bytes_of_any(p, cap)
+    plan->ws_any = ws_bytes_of_any(p, cap);
+    // (a window's kernel is chosen by estimates: its calls ask for ws_any)
+    plan->ws_bytes = win ? plan->ws_any
                          : ws_part_offset(p.S) + (size_t)2 * plan->grid * part_slot_floats(p) * sizeof(float);
     return TF_OK;
 }
@@ -739,13 +742,7 @@ size_t tf_paged_attn_workspace_bytes(const tf_kv_pool *pool, const tf_streams *s
     Plan plan;
     if (make_plan(pool, streams, n_q_heads, rows, 4096, false, &plan) != TF_OK)
         return 0;
-    size_t bytes = plan.ws_bytes;
-    // enough for a tree-verify call with the same arguments too
-    Plan tp;
-    if (rows <= 8 && make_plan(pool, streams, n_q_heads, rows, 8, true, &tp) == TF_OK &&
-        tp.ws_bytes > bytes)
-        bytes = tp.ws_bytes;
-    return bytes;
+    return plan.ws_any;
 }
 
 int tf_paged_attn_decode(const tf_kv_pool *pool, const tf_streams *streams, const void *q,
@@ -791,7 +788,7 @@ size_t tf_paged_attn_window_workspace_bytes(const tf_kv_pool *pool, const tf_str
     Plan plan;
     if (make_plan(pool, streams, n_q_heads, rows, 4096, false, &plan, &win) != TF_OK)
         return 0;
-    return plan.ws_bytes;
+    return plan.ws_any;
 }
 
 int tf_paged_attn_decode_window(const tf_kv_pool *pool, const tf_streams *streams, const void *q,

@@ -235,7 +235,8 @@ TF_API int tf_kv_pages_fork(const tf_kv_pages *pages, const int32_t *src_table,
  * fewer; at 0 the page is free) and hold -1.  first null: from entry 0; end
  * null: to the row's end (both null: the streams are dropped).  Rolling back
  * drafts frees the entries past the last one in use.  Entries of -1 are
- * passed over.  A range outside the row frees nothing of it (TF_DEV_BAD_LEN);
+ * passed over.  A first or end outside [0, table_stride] frees nothing of the
+ * row and sets TF_DEV_BAD_LEN (end at or before first is an empty range);
  * a page that is outside the pool, or that nobody holds, sets
  * TF_DEV_BAD_PAGE. */
 TF_API int tf_kv_pages_free(const tf_kv_pages *pages, int32_t *table, int32_t table_stride,

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const __grid_constant__
             first = __ldg(p.first + s);
         if (p.end)
             end = __ldg(p.end + s);
-        if (first < 0 || end > p.stride) {
+        if (first < 0 || first > p.stride || end < 0 || end > p.stride) {
             if (j == 0)
                 note(p.status, kDevBadLen);
             return;

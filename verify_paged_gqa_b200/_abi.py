@@ -83,13 +83,24 @@ class tf_kv_pages(ctypes.Structure):
                 ("page_size", ctypes.c_int32)]
 
 
+class _NoBinding:
+    """Stands where the compiled binding does not load: the calls that ctypes
+    marshals work without it, the others say what is missing."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs the compiled binding, which does not load ({self.why}): build it with "
+                          "`python -m verify_paged_gqa_b200.build` (there is no fallback path)")
+
+
 raw = ctypes.CDLL(library_path)
 try:
     from . import _binding
+    _binding.attach(library_path)
 except ImportError as e:
-    raise ImportError(f"the compiled binding does not load ({e}): build it with "
-                      "`python -m verify_paged_gqa_b200.build` (there is no fallback path)") from e
-_binding.attach(library_path)
+    _binding = _NoBinding(e)
 _P = ctypes.POINTER
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 raw.tf_kv_put_rows.argtypes = [_P(tf_kv_pool), _P(tf_streams), _vp, _vp, _i32, _vp]

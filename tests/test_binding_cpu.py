@@ -43,3 +43,18 @@ def test_calls_of_the_library_alone_need_no_binding(built):
         else:
             raise AssertionError("no error")
     """)
+
+
+def test_another_python_or_torch_rebuilds_the_binding(built, monkeypatch):
+    """_binding.so loads under the Python and torch it was compiled against
+    only; file times do not tell."""
+    made = []
+    assert built.up_to_date()
+    monkeypatch.setattr(built, "build_binding", lambda: made.append(1))
+    built.build()
+    assert made == []
+    import torch
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    assert not built.up_to_date()
+    built.build()
+    assert made == [1]

@@ -21,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "tfpaged")
 LIB = os.path.join(HERE, "libtfpaged.so")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_FOR = os.path.join(HERE, "_binding.so.for")   # the Python and torch it was compiled against
 SOURCES = ["tf_paged.cu", "kv_put.cu", "kv_rope.cu", "kv_copy.cu", "kv_pages.cu", "attn_simt.cu", "attn_win.cu",
            "attn_prompt.cu", "attn_pm.cu", "attn_merge.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -41,11 +42,25 @@ def _deps():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _newer_than_sources(path) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in _deps())
+
+
+def _interpreter() -> str:
+    """What _binding.so is compiled against: it loads under no other Python or torch."""
+    import torch
+    return f"{sys.implementation.cache_tag} torch {torch.__version__}"
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer_than_sources(BINDING) or not os.path.exists(BINDING_FOR):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    with open(BINDING_FOR) as f:
+        return f.read() == _interpreter()
+
+
+def up_to_date() -> bool:
+    return _newer_than_sources(LIB) and _binding_up_to_date()
 
 
 # host-compiler flags of the sanitizer build (one per -Xcompiler: nvcc splits
@@ -73,6 +88,9 @@ def build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(_interpreter())
+    os.replace(tmp, BINDING_FOR)
 
 
 def build(verbose: bool = False, force: bool = False, sanitize: bool = False) -> str:
@@ -80,7 +98,9 @@ def build(verbose: bool = False, force: bool = False, sanitize: bool = False) ->
     separate copy (_build/asan/libtfpaged_asan.so) whose host code carries
     AddressSanitizer and UndefinedBehaviorSanitizer (device code is
     unchanged; the process that loads it must preload libasan)."""
-    if not sanitize and not force and not verbose and up_to_date():
+    if not sanitize and not force and not verbose and _newer_than_sources(LIB):
+        if not _binding_up_to_date():
+            build_binding()
         return LIB
     build_dir = os.path.join(ROOT, "_build", "asan") if sanitize else BUILD
     lib = os.path.join(build_dir, "libtfpaged_asan.so") if sanitize else LIB
@@ -101,8 +121,6 @@ def build(verbose: bool = False, force: bool = False, sanitize: bool = False) ->
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = None if sanitize else ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
-        if binding is not None:
-            binding.result()
     log = "".join(out for _, out in results)
     with open(os.path.join(build_dir, "ptxas.log"), "w") as f:
         f.write(log)
@@ -115,6 +133,8 @@ def build(verbose: bool = False, force: bool = False, sanitize: bool = False) ->
     os.replace(tmp, lib)
     if verbose:
         sys.stdout.write(log)
+    if binding is not None:
+        binding.result()   # (the library is there whether or not it compiled)
     return lib
 
 

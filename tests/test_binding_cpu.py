@@ -58,3 +58,48 @@ def test_another_python_or_torch_rebuilds_the_binding(built, monkeypatch):
     assert not built.up_to_date()
     built.build()
     assert made == [1]
+
+
+FAKE = """
+#include <unistd.h>
+volatile int entered;
+int entered_now(void) { return entered; }
+int tf_kv_pages_free(void) {  /* a launch that waits, as one into a full queue does */
+    entered = 1;
+    for (int i = 0; i < 200 && entered == 1; ++i)
+        usleep(10000);
+    return entered == 2 ? 0 : 4;
+}
+void let_go(void) { entered = 2; }
+"""
+
+
+def test_other_threads_run_while_a_call_launches(built, tmp_path):
+    """A launch may wait for room in the stream's queue, and what makes room may
+    be a host function that another Python thread has to run."""
+    import re
+    import shutil
+    if shutil.which("gcc") is None:
+        pytest.skip("needs gcc")
+    with open(os.path.join(built.CSRC, "binding.cpp")) as f:
+        names = re.findall(r"^ +X\\((tf_\\w+)\\)".replace("\\\\", "\\"), f.read(), re.M)
+    assert "tf_kv_pages_free" in names
+    src, so = tmp_path / "fake.c", tmp_path / "libfake.so"
+    src.write_text(FAKE + "".join(f"int {n}(void) {{ return 0; }}\n" for n in names if n != "tf_kv_pages_free"))
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    python(f"""
+        import ctypes, threading, time
+        import torch
+        from verify_paged_gqa_b200 import _abi
+        _abi._binding.attach({str(so)!r})
+        fake = ctypes.CDLL({str(so)!r})
+        args = (torch.zeros(0, dtype=torch.int32), 16, torch.zeros((0, 3), dtype=torch.int32), None, None, None, 0)
+        got = []
+        t = threading.Thread(target=lambda: got.append(_abi._binding.tf_kv_pages_free(*args)))
+        t.start()
+        while not fake.entered_now() and t.is_alive():
+            time.sleep(0.001)
+        fake.let_go()
+        t.join()
+        assert got == [0], got
+    """)

@@ -251,8 +251,16 @@ Rows rows_of(const at::Tensor &t, int64_t S, int64_t W, int64_t heads, int64_t d
 
 // ---- the calls ------------------------------------------------------------------
 
+// Lets other Python threads run while the library enqueues a call's kernels, as
+// ctypes does: a launch waits while the stream's queue is full, and a host
+// function in that queue may need the interpreter.
+struct NoGil {
+    PyThreadState *const state = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 // Runs f(args) with the number of arguments checked and exceptions kept out of
-// the interpreter; the GIL is held (the calls only enqueue work).
+// the interpreter.
 template <Py_ssize_t N, class F>
 PyObject *guarded(PyObject *const *args, Py_ssize_t n, F f)
 {
@@ -294,12 +302,15 @@ PyObject *attn_window(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int32_t window = int_of(a[5], "window"), sinks = int_of(a[6], "sinks");
         const float scale = float_of(a[7]);
         void *stream = stream_of(dev, a[11]);
+        const void *qp = q.data_ptr();
         float *o = (float *)out.data_ptr();
+        void *w = ws.data_ptr();
+        const size_t w_bytes = ws.nbytes();
+        NoGil no_gil;
         if (kind == 0)
-            return lib.tf_paged_attn_decode_window(&pool, &st, q.data_ptr(), heads, window, sinks, scale, o,
-                                                   ws.data_ptr(), ws.nbytes(), stream);
+            return lib.tf_paged_attn_decode_window(&pool, &st, qp, heads, window, sinks, scale, o, w, w_bytes, stream);
         return (kind == 1 ? lib.tf_paged_attn_verify_window : lib.tf_paged_attn_prompt_window)(
-            &pool, &st, q.data_ptr(), heads, rows, window, sinks, scale, o, ws.data_ptr(), ws.nbytes(), stream);
+            &pool, &st, qp, heads, rows, window, sinks, scale, o, w, w_bytes, stream);
     });
 }
 
@@ -342,8 +353,10 @@ PyObject *put_rows_rope(PyObject *, PyObject *const *args, Py_ssize_t n)
         must(freq.data_ptr() == rope->inv_freq, "the rope's inv_freq has moved");
         dev.on(freq, "inv_freq");
         void *stream = stream_of(dev, a[12]);
-        return lib.tf_kv_put_rows_rope(&pool, &st, rope, (const int32_t *)pos.data_ptr(), q.data, q.stride, q_out,
-                                       heads, kr.data, kr.stride, vr.data, vr.stride, (int32_t)W, stream);
+        const auto *position = (const int32_t *)pos.data_ptr();
+        NoGil no_gil;
+        return lib.tf_kv_put_rows_rope(&pool, &st, rope, position, q.data, q.stride, q_out, heads, kr.data,
+                                       kr.stride, vr.data, vr.stride, (int32_t)W, stream);
     });
 }
 
@@ -359,6 +372,7 @@ PyObject *pages_fork(PyObject *, PyObject *const *args, Py_ssize_t n)
         int32_t *dst_lens = row_ints(a[6], dst.rows, "dst_lens", dev);
         uint32_t *status = status_of(a[7], dev);
         void *stream = stream_of(dev, a[8]);
+        NoGil no_gil;
         return lib.tf_kv_pages_fork(&pg, src.data, src.stride, lens, src.rows, parents, dst.rows, dst.data, dst.stride,
                                     dst_lens, status, stream);
     });
@@ -374,6 +388,7 @@ PyObject *pages_free(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int32_t *first = row_ints(a[3], t.rows, "first", dev), *end = row_ints(a[4], t.rows, "end", dev);
         uint32_t *status = status_of(a[5], dev);
         void *stream = stream_of(dev, a[6]);
+        NoGil no_gil;
         return lib.tf_kv_pages_free(&pg, t.data, t.stride, t.rows, first, end, status, stream);
     });
 }
@@ -389,6 +404,7 @@ PyObject *pages_free_window(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int32_t window = int_of(a[4], "window"), sinks = int_of(a[5], "sinks");
         uint32_t *status = status_of(a[6], dev);
         void *stream = stream_of(dev, a[7]);
+        NoGil no_gil;
         return lib.tf_kv_pages_free_window(&pg, t.data, t.stride, lens, t.rows, window, sinks, status, stream);
     });
 }
@@ -405,6 +421,7 @@ PyObject *pages_grow(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int32_t rows = int_of(a[4], "rows");
         uint32_t *status = status_of(a[6], dev);
         void *stream = stream_of(dev, a[7]);
+        NoGil no_gil;
         return lib.tf_kv_pages_grow(&pg, t.data, t.stride, lens, t.rows, rows, m.data, m.bytes, status, stream);
     });
 }
@@ -419,6 +436,7 @@ PyObject *pages_compact(PyObject *, PyObject *const *args, Py_ssize_t n)
         const Moves m = moves_of(a[3], dev);
         uint32_t *status = status_of(a[4], dev);
         void *stream = stream_of(dev, a[5]);
+        NoGil no_gil;
         return lib.tf_kv_pages_compact(&pg, t.data, t.stride, t.rows, m.data, m.bytes, status, stream);
     });
 }
@@ -432,6 +450,7 @@ PyObject *pages_move(PyObject *, PyObject *const *args, Py_ssize_t n)
         const Moves m = moves_of(a[2], dev);
         uint32_t *status = status_of(a[3], dev);
         void *stream = stream_of(dev, a[4]);
+        NoGil no_gil;
         return lib.tf_kv_pages_move(&pool, m.data, m.bytes, status, stream);
     });
 }

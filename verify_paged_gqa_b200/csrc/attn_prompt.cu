@@ -681,10 +681,19 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t strea
 }
 
 // Sliding windows start and end inside tiles: pieces at any page size.  Windows
-// of more than kFoldWindow positions fold: 2 streams x 4,096 rows x 32 heads
-// over 4,096 positions take 928 us without and 1,241 with, off by 5e-6 and 3e-6
-// of the output's norm; over 8,192 it would be 8e-6 without, and growing.
-constexpr int kFoldWindow = 4608;
+// of more than kFoldWindow positions fold.  Folding makes PV sixteen products of
+// N = 128 a tile, and the output's error 3.3e-6 of its norm at any length; without,
+// the error grows with the sums' truncation.  The budget is 6e-6: the 2^-17 that
+// these calls are tested to, less a fifth for sums that cancel little,
+// which 36 tiles stay within.  2 streams x 4,096 rows x 32 heads, us and error,
+// unfolded / folded:
+//   window 1,024    398 / 484    2.7e-6 / 3.1e-6
+//   window 2,048    589 / 725    3.4e-6 / 3.2e-6
+//   window 4,096    955 / 1,175  5.2e-6 / 3.3e-6
+//   window 4,600  1,011 / 1,203  5.7e-6 / 3.2e-6
+//   window 6,144  1,312 / 1,616  7.5e-6 / 3.3e-6
+//   window 8,192  1,678 / 2,071  9.8e-6 / 3.3e-6
+constexpr int kFoldWindow = 36 * PT;
 
 cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream)
 {

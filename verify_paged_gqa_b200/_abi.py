@@ -239,15 +239,28 @@ class Rope:
         self.address = ctypes.addressof(self.struct)
 
 
+def _empty_for(stream, like):
+    """A tensor of like's shape and type that a call on `stream` may write at
+    once: its memory comes from that stream's own freed blocks, which nothing on
+    another stream still uses."""
+    if stream is None or not like.is_cuda:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
 def tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, positions, rope, max_len,
                         q_out=None, stream=None):
     """Turns a step's rows q [S][W][Hq][d] and k_rows [S][W][Hkv][d] by their
     rotary positions (int32 [S][W][n_axes]) and writes k_rows and v_rows into
     their pages.  The rows may be slices of one projection's output.  Returns
     the turned queries (q_out, a new tensor by default, or q itself to turn
-    them in place); q may be None."""
+    them in place); q may be None.  A new tensor belongs to the call's stream:
+    used on another one, it is subject to torch's record_stream as any."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = _empty_for(stream, q)
     rc = _binding.tf_kv_put_rows_rope(k_pool, v_pool, table, lens, q, k_rows, v_rows, positions,
                                       rope.inv_freq, rope.address, max_len, q_out, stream)
     if rc:

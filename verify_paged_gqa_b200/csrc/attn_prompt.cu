@@ -23,8 +23,9 @@
 // plan.cuh.  P's parts are rounded to nearest instead (2^-18 of P, no bias), a
 // CTA takes whole row blocks, and their rows leave through shared memory while
 // the next block starts.  2 streams x 4,096 rows of 32 heads over a window of
-// 4,096: 928 us, 593 TFLOP/s of the products that the rows see; a tile takes
-// 1.5 us of it, a block beside its tiles 13 to 16.
+// 4,096: 936 us at full clock, 588 TFLOP/s of the products that the rows see
+// (1,041 us and 529 call after call, under the power cap); a tile takes 1.5 us
+// of it, a block beside its tiles 13 to 16.
 //
 // One persistent CTA per SM, ten warps:
 //   warp 0     producer (one lane): the K/V ring (ring.cuh).

@@ -3,8 +3,8 @@
 //
 // A window bounds what a block reads (window + sinks positions), so such a
 // call is short and what counts is its latency and that every SM has loads in
-// flight from the first microsecond on.  The kernel therefore has no producer,
-// no ring and no second launch:
+// flight from the first microsecond on.  The kernel therefore has no producer
+// warp, no ring that its warps share and no second launch:
 //
 //   split    a unit (stream, KV head, row block) is one cluster of C thread
 //            blocks; its positions are dealt out in chunks of 16 to the
@@ -38,8 +38,8 @@
 //
 // Measured: 12 streams of 32 query heads over a window of 4,096 38.7 us (5.2 TB/s:
 // one and a half waves of clusters, so the start and the join show), 64 ragged
-// streams over windows up to 8,192 in pages of 64 179 us (6.05 TB/s), one stream
-// and KV head over 256 positions 5.6 us.
+// streams over windows up to 8,192 in pages of 64 183 us (5.4 TB/s of the
+// positions they have), one stream and KV head over 256 positions 5.6 us.
 //
 // D = 256 and 512: a team is D / 128 warps that share positions and split the
 // dims; the chunk's scores are summed over the team through shared memory.

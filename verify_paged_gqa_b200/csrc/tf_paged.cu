@@ -149,8 +149,11 @@ int32_t window_pieces(int32_t head_dim, int64_t units, int64_t cap, int64_t tile
 // 256 units; windows of 64 to 8,192): the choice is 0.6% slower than the faster
 // of the two in the geometric mean, 28% at worst, where always the cluster
 // kernel up to 16 rows was 11%, never 25%.  Over 400 others, drawn over all page
-// sizes and ratios of heads, it was 0.5% (55% for one, over pages of 16).  In tenths of microseconds, without
-// what both take to start:
+// sizes and ratios of heads, it was 0.5%; at worst 55% (1,540 rows at head dim 512
+// over pages of 16: 888 us, 574 on the cluster kernel), 46% (7 rows at head dim
+// 256 over pages of 16) and 35% (one row of 3 streams at head dim 512 over pages
+// of 512: 30.5 us and 22.7).  In tenths of microseconds, without what both take to
+// start:
 //   cluster      its chunks one after another, 1.2 to 2.1 us each: it reads the
 //                unit again for every 16 rows, and its products run on mma.sync
 //                and FMAs

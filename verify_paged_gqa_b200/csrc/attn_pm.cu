@@ -1115,12 +1115,12 @@ cudaError_t launch_pm(const P &p, int grid, cudaStream_t stream)
 // kernel (tree calls run here with several row blocks), and pool rows are
 // addressed by 32-bit coordinates.  Any page size: tiles that straddle pages
 // are gathered row by row.
-int pm_rows(const AttnParams &p)
+int pm_rows(const AttnParams &p, bool any_count)
 {
     if (!pool_rows_fit(p))
         return 0;
     if (p.D == 128)
-        return p.M <= 32 ? 32 : (p.M <= 64 || p.has_tree) ? 64 : 0;
+        return p.M <= 32 ? 32 : (p.M <= 64 || any_count) ? 64 : 0;
     if (p.D == 256 || p.D == 512)
         return kPmWideRows;
     return 0;

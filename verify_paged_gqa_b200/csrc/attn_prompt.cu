@@ -24,7 +24,7 @@
 // CTA takes whole row blocks, and their rows leave through shared memory while
 // the next block starts.  2 streams x 4,096 rows of 32 heads over a window of
 // 4,096: 936 us at full clock, 588 TFLOP/s of the products that the rows see
-// (1,041 us and 529 call after call, under the power cap); a tile takes 1.5 us
+// (1,027 to 1,042 us and 529 to 536 call after call, under the power cap); a tile takes 1.5 us
 // of it, a block beside its tiles 13 to 16.
 //
 // One persistent CTA per SM, ten warps:
@@ -91,13 +91,9 @@ static_assert(kPrSmemBytes <= 232448, "shared memory");
 
 // Kernel arguments: the call's parameters and the K and V pools' tensor maps
 // (one 128-row box, or for tiles assembled from pages one map per box height).
-// The softmax takes a row's maximum over raw scores and masks them with -inf
-// before it scales them, so the scale it sees is positive: a negative one is
-// the queries' sign (q_flip), and one of zero queries of zero (q_keep).
 template <bool kG, class P>
 struct PrArgs {
     P p;
-    uint32_t q_keep, q_flip;  // a pair of query values is taken as (pair & q_keep) ^ q_flip
     CUtensorMap kmap[kG ? kBoxHeights : 1];
     CUtensorMap vmap[kG ? kBoxHeights : 1];
 };
@@ -216,7 +212,9 @@ __device__ __forceinline__ uint64_t low_bits(int n)
 // which are K-atom hh of the P tile.  During a tile a thread works on its
 // row's half; a row's two threads agree on the row's reference max (they
 // compute it from the same shared values).  In the epilogue the thread reads
-// O^T lane r (head dim r) for rows [64 hh, 64 hh + 64).
+// O^T lane r (head dim r) for rows [64 hh, 64 hh + 64).  A row's maximum is taken
+// over raw scores, and those are masked with -inf, before they are scaled: the
+// scale is positive (calls of any other run on attn_pm).
 template <bool kWin, bool kFold, class A>
 __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int lane)
 {
@@ -258,10 +256,10 @@ __device__ __forceinline__ void pr_softmax(const A &a, PrSmem &sm, int warp, int
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                qr[c * 4 + 0] = (v.x & a.q_keep) ^ a.q_flip;
-                qr[c * 4 + 1] = (v.y & a.q_keep) ^ a.q_flip;
-                qr[c * 4 + 2] = (v.z & a.q_keep) ^ a.q_flip;
-                qr[c * 4 + 3] = (v.w & a.q_keep) ^ a.q_flip;
+                qr[c * 4 + 0] = v.x;
+                qr[c * 4 + 1] = v.y;
+                qr[c * 4 + 2] = v.z;
+                qr[c * 4 + 3] = v.w;
             }
             // (the previous segment's last QK: complete in practice, its S was read)
             ok = pwait(sm, &sm.q_free, (j & 1u) ^ 1u, p.flags, kWaitQEmpty) && ok;
@@ -654,9 +652,6 @@ cudaError_t launch_prompt(const P &p, int grid, cudaStream_t stream)
 {
     PrArgs<kG, P> a;
     a.p = p;
-    a.q_keep = p.scale_log2 != 0.f ? 0xffffffffu : 0u;
-    a.q_flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    a.p.scale_log2 = p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
     // one box of a whole 128-position tile, or boxes of 1, 2, 4, ..., 128 rows
     // for tiles assembled from page pieces
     for (int h = 0; h < (kG ? kBoxHeights : 1); ++h) {
@@ -688,12 +683,12 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t strea
 // these calls are tested to, less a fifth for sums that cancel little,
 // which 36 tiles stay within.  2 streams x 4,096 rows x 32 heads, us and error,
 // unfolded / folded:
-//   window 1,024    398 / 484    2.7e-6 / 3.1e-6
-//   window 2,048    589 / 725    3.4e-6 / 3.2e-6
-//   window 4,096    955 / 1,175  5.2e-6 / 3.3e-6
-//   window 4,600  1,011 / 1,203  5.7e-6 / 3.2e-6
-//   window 6,144  1,312 / 1,616  7.5e-6 / 3.3e-6
-//   window 8,192  1,678 / 2,071  9.8e-6 / 3.3e-6
+//   window 1,024    397 / 489    2.7e-6 / 3.1e-6
+//   window 2,048    580 / 741    3.4e-6 / 3.2e-6
+//   window 4,096    936 / 1,205  5.2e-6 / 3.3e-6
+//   window 4,600    992 / 1,221  5.7e-6 / 3.2e-6
+//   window 6,144  1,294 / 1,665  7.5e-6 / 3.3e-6
+//   window 8,192  1,663 / 2,136  9.8e-6 / 3.3e-6
 constexpr int kFoldWindow = 36 * PT;
 
 cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream)

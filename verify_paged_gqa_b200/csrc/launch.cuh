@@ -167,10 +167,11 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t strea
 cudaError_t launch_attn_prompt(const WinParams &p, int grid, cudaStream_t stream);
 
 // Position-major tensor-core partial kernel: key positions on the MMA's M,
-// row blocks of pm_rows(p) rows (0: not supported for these arguments),
-// kPmWideRows at head dims 256 and 512.
+// row blocks of pm_rows() rows (0: not supported for these arguments), kPmWideRows
+// at head dims 256 and 512.  More than 64 rows per KV head at head dim 128 are
+// the prompt kernel's, unless `any_count`.
 constexpr int kPmWideRows = 32;
-int pm_rows(const AttnParams &p);
+int pm_rows(const AttnParams &p, bool any_count);
 cudaError_t launch_attn_pm(const AttnParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_attn_pm(const WinParams &p, int grid, cudaStream_t stream);
 

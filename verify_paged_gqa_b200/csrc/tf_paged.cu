@@ -200,7 +200,7 @@ bool takes_win_kernel(WinParams &p, int sms, int forced)
 }
 
 int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t rows,
-              int32_t rows_max, bool tree, Plan *plan, const Window *win = nullptr)
+              int32_t rows_max, bool tree, Plan *plan, float scale = 1.f, const Window *win = nullptr)
 {
     int rc = check_pool_streams(pool, st);
     if (rc != TF_OK)
@@ -266,11 +266,16 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     // 5,187; 12 x 40,960 6,875 / 6,061).  max_len bounds every stream, so the
     // choice depends on host arguments only.
     const bool long_context = st->max_len >= kPmDecodeMinLen;
+    // The prompt kernel knows no tree masks, and takes positive scales only: it
+    // masks raw scores.  Blocks of 64 rows on the position-major kernel do both
+    // (the signs in its queries' loads, which the prompt kernel would take at its
+    // registers' limit, cost every call of it 0.7 to 2.2%).
+    const bool pm_only = tree || !(scale > 0.f);
     plan->kernel = Kernel::kSimt;
     p.RB = kSimtRows;
     if (win) {
         // a sliding window; pools past 2^31 rows are refused
-        const int nr = pm_rows(p);
+        const int nr = pm_rows(p, pm_only);
         if (pool_rows_past_31_bits(pool))
             return TF_EUNSUPPORTED;
         int sms = 0;
@@ -291,7 +296,7 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
     } else if (tree) {
         // tree masks: the position-major kernel (any row count), else the
         // CUDA-core kernel (pools past 2^31 rows)
-        const int nr = pm_rows(p);
+        const int nr = pm_rows(p, pm_only);
         if (nr > 0) {
             plan->kernel = Kernel::kPm;
             p.RB = nr;
@@ -300,13 +305,13 @@ int make_plan(const tf_kv_pool *pool, const tf_streams *st, int32_t Hq, int32_t 
         }
     } else if (p.D == 256) {
         // head dim 256 runs on the position-major kernel only (any row count)
-        const int nr = pm_rows(p);
+        const int nr = pm_rows(p, pm_only);
         if (nr == 0)
             return TF_EUNSUPPORTED;
         plan->kernel = Kernel::kPm;
         p.RB = nr;
     } else if (M > kSimtRows || (p.D == 128 && !small_odd_pages && long_context)) {
-        const int nr = pm_rows(p);
+        const int nr = pm_rows(p, pm_only);
         if (nr > 0) {
             plan->kernel = Kernel::kPm;
             p.RB = nr;
@@ -383,7 +388,7 @@ int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32
               const Window *win = nullptr)
 {
     Plan plan;
-    int rc = make_plan(pool, st, Hq, rows, rows_max, tree != nullptr, &plan, win);
+    int rc = make_plan(pool, st, Hq, rows, rows_max, tree != nullptr, &plan, scale, win);
     if (rc != TF_OK)
         return rc;
     plan.p.wait_limit = faults.wait_limit;
@@ -789,7 +794,7 @@ size_t tf_paged_attn_window_workspace_bytes(const tf_kv_pool *pool, const tf_str
 {
     const Window win{window, sinks, 0};
     Plan plan;
-    if (make_plan(pool, streams, n_q_heads, rows, 4096, false, &plan, &win) != TF_OK)
+    if (make_plan(pool, streams, n_q_heads, rows, 4096, false, &plan, 1.f, &win) != TF_OK)
         return 0;
     return plan.ws_any;
 }
@@ -940,7 +945,7 @@ extern "C" int tf_paged_attn_decode_noalloc(const tf_kv_pool *pool, const tf_str
 {
     using namespace tfp;
     Plan plan;
-    int rc = make_plan(pool, streams, n_q_heads, 1, 1, false, &plan);
+    int rc = make_plan(pool, streams, n_q_heads, 1, 1, false, &plan, scale);
     if (rc != TF_OK)
         return rc;
     if (!std::isfinite(scale))

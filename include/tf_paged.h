@@ -30,6 +30,9 @@
  *    out             fp32  [n_streams][rows][n_q_heads][head_dim]       device
  *    k_rows, v_rows  bf16  [n_streams][rows][n_kv_heads][head_dim]      device
  *
+ *  (pools, q, out and rows 16-byte aligned; every array of 32-bit values
+ *  4-byte aligned)
+ *
  *  lens[s] counts the positions of stream s AFTER this step's rows are
  *  written.  Window row r (0 <= r < rows) sits at position
  *  lens[s] - rows + r and attends to positions 0 .. lens[s] - rows + r.
@@ -79,7 +82,7 @@ extern "C" {
 
 /* Status codes returned by every call. */
 #define TF_OK 0
-#define TF_EINVAL 1        /* a NULL pointer, a bad size or an inconsistent shape */
+#define TF_EINVAL 1        /* a NULL or misaligned pointer, a bad size or an inconsistent shape */
 #define TF_EUNSUPPORTED 2  /* a shape this library has no kernel for (head_dim, page_size) */
 #define TF_ENOSPACE 3      /* the workspace (or list) is too small for the call */
 #define TF_ECUDA 4         /* a CUDA launch or query failed */

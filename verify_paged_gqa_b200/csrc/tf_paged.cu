@@ -38,6 +38,7 @@ int device_sm_count(int *sms)
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_pool_streams(const tf_kv_pool *pool, const tf_streams *st)
 {
@@ -53,7 +54,7 @@ int check_pool_streams(const tf_kv_pool *pool, const tf_streams *st)
         return TF_EINVAL;
     if ((int64_t)st->n_streams * st->table_stride > INT32_MAX)
         return TF_EINVAL;
-    if (st->n_streams > 0 && (!st->table || !st->lens))
+    if (st->n_streams > 0 && (!st->table || !st->lens || !aligned4(st->table) || !aligned4(st->lens)))
         return TF_EINVAL;
     if (!pool->k_pool || !pool->v_pool || !aligned16(pool->k_pool) || !aligned16(pool->v_pool))
         return TF_EINVAL;
@@ -435,8 +436,6 @@ int attn_call(const tf_kv_pool *pool, const tf_streams *st, const void *q, int32
     return e == cudaSuccess ? TF_OK : TF_ECUDA;
 }
 
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 // Pages and entries of a table row at most: the kernels step past the last
 // one by up to a block's 4,096, in 32 bits.
 constexpr int32_t kMaxPages = INT32_MAX - 8192;
@@ -540,8 +539,8 @@ int tf_kv_put_rows_rope(const tf_kv_pool *pool, const tf_streams *streams, const
         return TF_EINVAL;
     if (streams->n_streams == 0)
         return TF_OK;
-    if (!rope->inv_freq || !positions || !k_rows || !v_rows || !aligned16(k_rows) ||
-        !aligned16(v_rows))
+    if (!rope->inv_freq || !aligned4(rope->inv_freq) || !positions || !aligned4(positions) || !k_rows ||
+        !v_rows || !aligned16(k_rows) || !aligned16(v_rows))
         return TF_EINVAL;
     if (n_q_heads > 0 && (!q || !q_out || !aligned16(q) || !aligned16(q_out)))
         return TF_EINVAL;
@@ -591,9 +590,9 @@ int tf_kv_copy_state(const tf_kv_pool *src_pool, const tf_streams *src,
         (int64_t)src->max_len > (int64_t)dst_table_stride * dst_pool->page_size ||
         (int64_t)src->n_streams * dst_table_stride > INT32_MAX)
         return TF_EINVAL;
-    if (src->n_streams > 0 && !dst_table)
+    if (src->n_streams > 0 && (!dst_table || !aligned4(dst_table)))
         return TF_EINVAL;
-    if (status && (reinterpret_cast<uintptr_t>(status) & 3u) != 0)
+    if (!aligned4(status))
         return TF_EINVAL;
     if (src->n_streams == 0)
         return TF_OK;
@@ -634,11 +633,12 @@ int tf_kv_pages_fork(const tf_kv_pages *pages, const int32_t *src_table, int32_t
     if (n_dst < 0 || dst_stride < 1 || dst_stride > kMaxPages ||
         (int64_t)n_dst * dst_stride > INT32_MAX)
         return TF_EINVAL;
-    if (n_src > 0 && !src_lens)
+    if (n_src > 0 && (!src_lens || !aligned4(src_lens)))
         return TF_EINVAL;
     if (n_dst == 0)
         return TF_OK;
-    if (!parents || !dst_table || !dst_lens)
+    if (!parents || !dst_table || !dst_lens || !aligned4(parents) || !aligned4(dst_table) ||
+        !aligned4(dst_lens))
         return TF_EINVAL;
     p.lens = src_lens;
     p.parents = parents;
@@ -656,6 +656,8 @@ int tf_kv_pages_free(const tf_kv_pages *pages, int32_t *table, int32_t table_str
     const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
     if (rc != TF_OK || n_streams == 0)
         return rc;
+    if (!aligned4(first) || !aligned4(end))
+        return TF_EINVAL;
     p.first = first;
     p.end = end;
     return status_of(launch_pages_free(p, false, static_cast<cudaStream_t>(stream)));
@@ -669,7 +671,7 @@ int tf_kv_pages_free_window(const tf_kv_pages *pages, int32_t *table, int32_t ta
     const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
     if (rc != TF_OK)
         return rc;
-    if (window < 1 || sinks < 0 || (n_streams > 0 && !lens))
+    if (window < 1 || sinks < 0 || (n_streams > 0 && (!lens || !aligned4(lens))))
         return TF_EINVAL;
     if (n_streams == 0)
         return TF_OK;
@@ -687,7 +689,7 @@ int tf_kv_pages_grow(const tf_kv_pages *pages, int32_t *table, int32_t table_str
     const int rc = check_pages(pages, table, table_stride, n_streams, status, &p);
     if (rc != TF_OK)
         return rc;
-    if (rows < 1 || (n_streams > 0 && !lens) || !moves || !aligned16(moves))
+    if (rows < 1 || (n_streams > 0 && (!lens || !aligned4(lens))) || !moves || !aligned16(moves))
         return TF_EINVAL;
     const int64_t per_stream = ((int64_t)rows + p.P - 2) / p.P + 1;
     const int64_t cap = move_cap(moves_bytes);

@@ -41,9 +41,9 @@
  *
  *  The output is softmax(scale * q . k) weighted sum of v, accumulated in
  *  fp32 from bf16 inputs; scale is any finite number (TF_EINVAL otherwise),
- *  zero and negative ones included.  Which pool pages hold a stream's positions never
- *  changes a bit of the result: the arithmetic depends only on positions,
- *  lens, rows and the host arguments.
+ *  zero and negative ones included.  Which pool pages hold a stream's
+ *  positions never changes a bit of the result: the arithmetic depends only
+ *  on positions, lens, rows and the host arguments.
  *
  *  Ownership: the caller owns every buffer.  The library allocates nothing
  *  and keeps no state between calls; each call enqueues kernels on the
@@ -389,8 +389,8 @@ TF_API int tf_paged_attn_prompt(const tf_kv_pool *pool, const tf_streams *stream
  * calls.  Accuracy, relative to the output's norm: 5e-7 for up to 16 rows per KV
  * head where they run on CUDA cores and mma.sync, 3.5e-6 on the tensor cores
  * (weights kept in two bf16 parts), growing to 6e-6 for prompt rows of head dim
- * 128 over windows from 1,024 to 4,608 positions.  TF_EUNSUPPORTED for pools of more than 2^31 - 1 rows (n_pages *
- * n_kv_heads * page_size).  The workspace is sized by its own call, since a
+ * 128 over windows from 1,024 to 4,608 positions.  TF_EUNSUPPORTED for pools
+ * of more than 2^31 - 1 rows (n_pages * n_kv_heads * page_size).  The workspace is sized by its own call, since a
  * window may be split over other kernels than the whole context; one
  * workspace of the larger size serves both kinds of layer in turn.  The figure
  * grows with n_streams and with rows * n_q_heads and does not depend on

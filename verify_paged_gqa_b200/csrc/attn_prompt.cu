@@ -24,8 +24,8 @@
 // CTA takes whole row blocks, and their rows leave through shared memory while
 // the next block starts.  2 streams x 4,096 rows of 32 heads over a window of
 // 4,096: 936 us at full clock, 588 TFLOP/s of the products that the rows see
-// (1,027 to 1,042 us and 529 to 536 call after call, under the power cap); a tile takes 1.5 us
-// of it, a block beside its tiles 13 to 16.
+// (1,027 to 1,042 us and 529 to 536 call after call, under the power cap); a
+// tile takes 1.5 us of it, a block beside its tiles 13 to 16.
 //
 // One persistent CTA per SM, ten warps:
 //   warp 0     producer (one lane): the K/V ring (ring.cuh).
@@ -679,10 +679,10 @@ cudaError_t launch_attn_prompt(const AttnParams &p, int grid, cudaStream_t strea
 // Sliding windows start and end inside tiles: pieces at any page size.  Windows
 // of more than kFoldWindow positions fold.  Folding makes PV sixteen products of
 // N = 128 a tile, and the output's error 3.3e-6 of its norm at any length; without,
-// the error grows with the sums' truncation.  The budget is 6e-6: the 2^-17 that
-// these calls are tested to, less a fifth for sums that cancel little,
-// which 36 tiles stay within.  2 streams x 4,096 rows x 32 heads, us and error,
-// unfolded / folded:
+// the error grows with the sums' truncation.  The budget is 6e-6 (the 2^-17 that
+// these calls are tested to, less a fifth for sums that cancel little), which 36
+// tiles stay within.  2 streams x 4,096 rows x 32 heads, us and error, unfolded /
+// folded:
 //   window 1,024    397 / 489    2.7e-6 / 3.1e-6
 //   window 2,048    580 / 741    3.4e-6 / 3.2e-6
 //   window 4,096    936 / 1,205  5.2e-6 / 3.3e-6

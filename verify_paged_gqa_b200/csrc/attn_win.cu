@@ -38,7 +38,7 @@
 //
 // Measured: 12 streams of 32 query heads over a window of 4,096 38.7 us (5.2 TB/s:
 // one and a half waves of clusters, so the start and the join show), 64 ragged
-// streams over windows up to 8,192 in pages of 64 183 us (5.4 TB/s of the
+// streams over windows up to 8,192 in pages of 64 180 us (5.4 TB/s of the
 // positions they have), one stream and KV head over 256 positions 5.6 us.
 //
 // D = 256 and 512: a team is D / 128 warps that share positions and split the

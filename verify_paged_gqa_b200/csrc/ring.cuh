@@ -323,8 +323,8 @@ __device__ __forceinline__ void ring_producer_pieces(const P &p, const CUtensorM
 // loses a little towards zero at every product: 1.2e-6 of the output's norm per
 // 1,000 positions, beside the 2.3e-6 that P's two bf16 parts leave.  A folding
 // kernel adds O^T to a second accumulator in fp32, with rounding, every
-// kFoldTiles tiles and starts it anew: 3.4e-6 in all (as squares) at any length.  attn_pm folds
-// every sliding window, attn_prompt those past its kFoldWindow.
+// kFoldTiles tiles and starts it anew: 3.4e-6 in all at any length.  attn_pm
+// folds every sliding window, attn_prompt those past its kFoldWindow.
 constexpr int kFoldTiles = 8;
 
 // Whether the PV product of a segment's tile t adds to O^T (else it starts it).
